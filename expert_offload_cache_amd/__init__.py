@@ -11,13 +11,14 @@ from typing import Optional
 
 import numpy as np
 
-from ._lib import (MOE_BF16, MOE_F32, MOE_INT4_G128, MoeError, check, lib)
+from ._lib import (MOE_BF16, MOE_F32, MOE_FP8_B128, MOE_INT4_G128, MoeError, check, lib)
 
-__all__ = ["route", "permute", "permute_workspace", "permute_workspace_bytes", "route_permute", "expert_ffn_grouped", "expert_ffn_grouped_noalloc", "combine",
+__all__ = ["route", "permute", "permute_workspace", "permute_workspace_bytes", "route_permute", "expert_ffn_grouped", "expert_ffn_grouped_noalloc", "expert_ffn_fp8", "combine",
+           "add_rmsnorm", "quant_fp8", "gemm_fp8",
            "slot_bytes", "pack_expert", "workspace_bytes", "hybrid_split", "SlotCache", "pinned_alloc", "pinned_free", "profile_enable",
            "profile_collect", "profile_results", "profile_reset", "MoeError", "WDT", "lib"]
 
-WDT = {"f32": MOE_F32, "bf16": MOE_BF16, "int4": MOE_INT4_G128}
+WDT = {"f32": MOE_F32, "bf16": MOE_BF16, "int4": MOE_INT4_G128, "fp8": MOE_FP8_B128}
 
 
 def _torch():
@@ -171,6 +172,130 @@ def expert_ffn_grouped_noalloc(x, perm, offsets, counts, slot_of_expert, slot_po
                                                _p(slot_of_expert), n_slots, _p(slot_pool), slot_stride, WDT[wdt],
                                                _p(shared_w), _p(y_perm), _y_code(y_perm), _p(status), _s(stream)))
     return y_perm
+
+
+def _on_current_device(*ts):
+    """The library launches on the current device: every tensor has to live there."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _rows(name, t, T: int, d: int, dtype) -> int:
+    """Checks a [T, d] tensor of dense rows; -> elements from a row to the next."""
+    if t.dtype != dtype or tuple(t.shape) != (T, d):
+        raise ValueError(f"{name} must be {dtype} [{T}, {d}], got {t.dtype} {list(t.shape)}")
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must lie next to each other")
+    return t.stride(0) if T > 1 else d
+
+
+def _dense(name, t, shape, dtype):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _quantised_out(x, T: int, d: int, out):
+    torch = _torch()
+    if out[0] is None:
+        out = (torch.empty((T, d), dtype=torch.float8_e4m3fn, device=x.device),
+               torch.empty((T, (d + 127) // 128), dtype=torch.float32, device=x.device))
+    q, scale = out
+    ldq = _rows("q", q, T, d, torch.float8_e4m3fn)
+    _dense("scale", scale, (T, (d + 127) // 128), torch.float32)
+    return q, scale, ldq
+
+
+def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, emit: str = "y", out=None, stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, rows [T, d] (moe_add_rmsnorm).
+    emit: "y" (rows in x's type), "fp8" (e4m3 rows and their scales) or "both".
+    out: the returned tuple's tensors to write into (None where not emitted).
+    -> (y, h, q, scale), None where there is none (h: without a residual)."""
+    torch = _torch()
+    if emit not in ("y", "fp8", "both"):
+        raise ValueError(f'emit must be "y", "fp8" or "both", got {emit!r}')
+    act = _act(x)
+    T, d = x.shape
+    y, h, q, scale = out if out is not None else (None, None, None, None)
+    if out is None and emit != "fp8":
+        y = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    if out is None and residual is not None:
+        h = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    ldq = 0
+    if emit != "y":
+        q, scale, ldq = _quantised_out(x, T, d, (q, scale))
+    elif q is not None or scale is not None:
+        raise ValueError('out holds q or scale, but emit is "y"')
+    if (y is None) != (emit == "fp8"):
+        raise ValueError(f"emit {emit!r} and out's y do not agree")
+    if (residual is None) != (h is None):
+        raise ValueError("a residual and its sum in out come together")
+    _on_current_device(x, weight, residual, y, h, q, scale)
+    w_code = act if weight.dtype == x.dtype else MOE_F32
+    _dense("weight", weight, (d,), x.dtype if w_code == act else torch.float32)
+    check(lib().moe_add_rmsnorm(_p(x), act, T, d, _rows("x", x, T, d, x.dtype), _p(residual),
+                                0 if residual is None else _rows("residual", residual, T, d, x.dtype), _p(weight), w_code,
+                                eps, _p(h), 0 if h is None else _rows("h", h, T, d, x.dtype), _p(y),
+                                0 if y is None else _rows("y", y, T, d, x.dtype), _p(q), ldq, _p(scale), _s(stream)))
+    return y, h, q, scale
+
+
+def quant_fp8(x, out=None, stream=None):
+    """Rows [T, d] -> (q e4m3 [T, d], scale f32 [T, ceil(d / 128)]) (moe_quant_fp8)."""
+    act = _act(x)
+    T, d = x.shape
+    q, scale, ldq = _quantised_out(x, T, d, out if out is not None else (None, None))
+    _on_current_device(x, q, scale)
+    check(lib().moe_quant_fp8(_p(x), act, T, d, _rows("x", x, T, d, x.dtype), _p(q), ldq, _p(scale), _s(stream)))
+    return q, scale
+
+
+def gemm_fp8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None):
+    """c [M, N] = rows a (e4m3 [M, K], scales [M, ceil(K/128)]) times w transposed (e4m3 [N, K],
+    scales [ceil(N/128), ceil(K/128)]) (moe_gemm_fp8).  out_dtype: bfloat16 (default) or float32."""
+    torch = _torch()
+    M, K = a.shape
+    N = w.shape[0]
+    G = (K + 127) // 128
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, not {out_dtype}")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the result must be bfloat16 or float32, got {out.dtype}")
+    lda, ldw = _rows("a", a, M, K, torch.float8_e4m3fn), _rows("w", w, N, K, torch.float8_e4m3fn)
+    _dense("a_scale", a_scale, (M, G), torch.float32)
+    _dense("w_scale", w_scale, ((N + 127) // 128, G), torch.float32)
+    _on_current_device(a, a_scale, w, w_scale, out)
+    check(lib().moe_gemm_fp8(_p(a), lda, _p(a_scale), M, K, _p(w), ldw, _p(w_scale), N, _p(out),
+                             _rows("out", out, M, N, out.dtype), MOE_BF16 if out.dtype == torch.bfloat16 else MOE_F32,
+                             _s(stream)))
+    return out
+
+
+def expert_ffn_fp8(x, x_scale, perm, offsets, counts, slot_of_expert, slot_pool, n_slots: int, slot_stride: int,
+                   f: int, k: int, shared_w=None, y_perm=None, ws=None, stream=None, y_dtype=None):
+    """expert_ffn_grouped with fp8 weights for quantised rows: x e4m3 [T, d], x_scale f32 [T, d/128]
+    (moe_expert_ffn_fp8). -> (y_perm [T*k (+T), d], ws).  y_perm float32 (default) or bfloat16."""
+    torch = _torch()
+    T, d = x.shape
+    E = counts.shape[0]
+    _dense("x", x, (T, d), torch.float8_e4m3fn)
+    _dense("x_scale", x_scale, (T, (d + 127) // 128), torch.float32)
+    rows = T * k + (T if shared_w is not None else 0)
+    if y_perm is None:
+        y_perm = torch.empty((rows, d), dtype=y_dtype or torch.float32, device=x.device)
+    if ws is None:
+        ws = torch.zeros(workspace_bytes(T, d, f, E, k, shared_w is not None, MOE_BF16, MOE_FP8_B128),
+                         dtype=torch.uint8, device=x.device)
+    _contig(perm, offsets, counts, slot_of_expert, y_perm)
+    _on_current_device(x, x_scale, perm, offsets, counts, slot_of_expert, slot_pool, shared_w, y_perm, ws)
+    check(lib().moe_expert_ffn_fp8(_p(x), _p(x_scale), T, d, f, E, k, _p(perm), _p(offsets), _p(counts),
+                                   _p(slot_of_expert), n_slots, _p(slot_pool), slot_stride, _p(shared_w), _p(y_perm),
+                                   _y_code(y_perm), _p(ws), ws.numel(), _s(stream)))
+    return y_perm, ws
 
 
 def combine(y_perm, topk_w, inv_perm, k: int, has_shared: bool, out_dtype, y=None, stream=None):

@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MOE_LIB_PATH") or os.path.join(HERE, "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_ESHAPE, MOE_EDTYPE, MOE_ENOMEM, MOE_EHIP, MOE_ECAPACITY, MOE_ESTATE = 0, -1, -2, -3, -4, -5, -6, -7
-MOE_F32, MOE_BF16, MOE_INT4_G128 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_INT4_G128, MOE_FP8_B128 = 0, 1, 2, 3
 STATUS_NAMES = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ESHAPE", -3: "MOE_EDTYPE", -4: "MOE_ENOMEM",
                 -5: "MOE_EHIP", -6: "MOE_ECAPACITY", -7: "MOE_ESTATE"}
 
@@ -30,6 +30,12 @@ SIGNATURES = {
                                      _i32, _vp, _vp, _i32, _vp, _sz, _vp]),
     "moe_expert_ffn_grouped_noalloc": (_st, [_vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32,
                                              _vp, _sz, _i32, _vp, _vp, _i32, _vp, _vp]),
+    "moe_expert_ffn_fp8": (_st, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp, _vp,
+                                 _i32, _vp, _sz, _vp]),
+    "moe_add_rmsnorm": (_st, [_vp, _i32, _i32, _i32, _sz, _vp, _sz, _vp, _i32, ctypes.c_float, _vp, _sz, _vp, _sz, _vp,
+                              _sz, _vp, _vp]),
+    "moe_quant_fp8": (_st, [_vp, _i32, _i32, _i32, _sz, _vp, _sz, _vp, _vp]),
+    "moe_gemm_fp8": (_st, [_vp, _sz, _vp, _i32, _i32, _vp, _sz, _vp, _i32, _vp, _sz, _i32, _vp]),
     "moe_prefill_gemv_tokens": (_i32, [_i32]),
     "moe_combine": (_st, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp]),
     "moe_decode_step": (_st, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _sz, _vp, _vp, _vp,

@@ -279,6 +279,7 @@ extern "C" moe_status moe_decode_step_hybrid(
               "moe_decode_step_hybrid: NULL pointer");
     MOE_CHECK(n_layers >= 0 && k >= 1 && k <= E && act == MOE_BF16, MOE_ESHAPE,
               "moe_decode_step_hybrid: need n_layers >= 0, 1 <= k <= E and bf16 activations");
+    MOE_CHECK(w != MOE_FP8_B128, MOE_EDTYPE, "moe_decode_step_hybrid: the host path has no fp8 experts");
     MOE_CHECK(pcie_rate > 0.0 && cpu_rate >= 0.0 && host_fixed_s >= 0.0, MOE_EINVAL,
               "moe_decode_step_hybrid: need pcie_rate > 0, cpu_rate >= 0, host_fixed_s >= 0");
     hipStream_t cs = (hipStream_t)compute;

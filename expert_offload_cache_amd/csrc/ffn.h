@@ -44,11 +44,11 @@ inline int64_t work_items(const FfnArgs& a, int ntg) {
 
 // Argument checks of moe_expert_ffn_grouped except the workspace; fills every field of `a` but
 // status, plan and h (left NULL).  T == 0 returns MOE_OK with nothing to run.  `fn` names the
-// caller in error messages.
+// caller in error messages.  rows8: x holds e4m3 rows (act is ignored; moe_expert_ffn_fp8 only).
 moe_status ffn_prepare(FfnArgs& a, const char* fn, const void* x, moe_dtype act, int T, int d, int f, int E, int k,
                        const int32_t* perm, const int32_t* offsets, const int32_t* counts,
                        const int32_t* slot_of_expert, int n_slots, const void* slot_pool, size_t slot_stride,
-                       moe_dtype w, const void* shared_w, void* y_perm, moe_dtype y_dtype);
+                       moe_dtype w, const void* shared_w, void* y_perm, moe_dtype y_dtype, bool rows8 = false);
 // Launch the grouped experts: the prefill MFMA GEMM where it applies, else the decode GEMVs.
 moe_status ffn_run(const FfnArgs& a, moe_dtype act, moe_dtype w, hipStream_t st);
 // moe_expert_ffn_grouped with the absent-slot flag going to `status` (device int32) instead of the

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include "ffn.h"
+#include "fp8_ops.h"
 #include "slot_layout.h"
 
 using namespace moe;
@@ -19,14 +20,16 @@ namespace moe {
 moe_status ffn_prepare(FfnArgs& a, const char* fn, const void* x, moe_dtype act, int T, int d, int f, int E, int k,
                        const int32_t* perm, const int32_t* offsets, const int32_t* counts,
                        const int32_t* slot_of_expert, int n_slots, const void* slot_pool, size_t slot_stride,
-                       moe_dtype w, const void* shared_w, void* y_perm, moe_dtype y_dtype) {
+                       moe_dtype w, const void* shared_w, void* y_perm, moe_dtype y_dtype, bool rows8) {
     MOE_CHECK(T >= 0, MOE_ESHAPE, "%s: T=%d < 0", fn, T);
     if (T == 0) return MOE_OK;
-    MOE_CHECK(act == MOE_F32 || act == MOE_BF16, MOE_EDTYPE, "%s: bad activation dtype", fn);
+    MOE_CHECK(rows8 || act == MOE_F32 || act == MOE_BF16, MOE_EDTYPE, "%s: bad activation dtype", fn);
     MOE_CHECK(w != MOE_INT4_G128 || act == MOE_BF16, MOE_EDTYPE, "%s: int4 needs bf16 activations", fn);
-    MOE_CHECK(w == MOE_INT4_G128 || w == act, MOE_EDTYPE, "%s: dense weights must have the activation dtype", fn);
-    MOE_CHECK(y_dtype == MOE_F32 || (y_dtype == MOE_BF16 && act == MOE_BF16), MOE_EDTYPE,
-              "%s: y_perm must be F32, or BF16 with bf16 activations", fn);
+    MOE_CHECK(w != MOE_FP8_B128 || rows8 || act == MOE_BF16, MOE_EDTYPE, "%s: fp8 weights need bf16 activations", fn);
+    MOE_CHECK(w == MOE_INT4_G128 || w == MOE_FP8_B128 || w == act, MOE_EDTYPE,
+              "%s: dense weights must have the activation dtype", fn);
+    MOE_CHECK(y_dtype == MOE_F32 || (y_dtype == MOE_BF16 && (rows8 || act == MOE_BF16)), MOE_EDTYPE,
+              "%s: y_perm must be F32, or BF16 with bf16 or fp8 activations", fn);
     MOE_CHECK(slot_shape_ok(d, f, w), MOE_ESHAPE, "%s: unsupported d=%d f=%d for dtype %d", fn, d, f, (int)w);
     MOE_CHECK(E >= 1 && E <= 1024 && k >= 1 && k <= E, MOE_ESHAPE, "%s: need 1 <= k <= E <= 1024", fn);
     MOE_CHECK((int64_t)T * k <= (1 << 24), MOE_ESHAPE, "%s: T*k too large", fn);
@@ -89,6 +92,7 @@ static int prefill_split_for(const FfnArgs& a, moe_dtype w) {
 }
 
 moe_status ffn_run(const FfnArgs& a, moe_dtype act, moe_dtype w, hipStream_t st) {
+    if (w == MOE_FP8_B128) return ffn_fp8_run(FfnFp8{a, nullptr}, st);
     // Prefill with few tokens on most experts: the experts holding fewer than `split` tokens go to
     // the decode kernels (their weights are streamed once, no 128-token tiles to fill), the others
     // and the shared expert to the matrix-core GEMM; both gate/up launches precede both down
@@ -122,10 +126,9 @@ int moe_prefill_gemv_tokens(moe_dtype w) {
 }
 
 size_t moe_workspace_bytes(int T, int d, int f, int E, int k, int has_shared, moe_dtype act, moe_dtype w) {
-    (void)d;
     (void)E;
-    (void)w;
     if (T < 0 || f <= 0 || k <= 0) return 0;
+    if (w == MOE_FP8_B128) return ffn_fp8_workspace(T, d, f, k, has_shared);
     return kWsHeader + kPlanBytes + h_bytes(T, f, k, has_shared, act);
 }
 

@@ -158,14 +158,28 @@ static void pack_int4_block(const uint8_t* q, const uint16_t* sc, int rb, int K,
     for (int r = 0; r < 16; ++r) memcpy(sdst + r * G, sc + (size_t)(rb * 16 + r) * G, (size_t)G * 2);
 }
 
+// one 16-row block of an fp8 [R, K] matrix: K/128 fragments of two halves, then the K/128 scales of
+// its 128 rows, padded to 64 bytes
+static void pack_fp8_block(const uint8_t* q, const float* sc, int rb, int K, uint8_t* blk) {
+    const int G = K / 128;
+    for (int g = 0; g < G; ++g)
+        for (int h = 0; h < 2; ++h)
+            for (int l = 0; l < 64; ++l)
+                memcpy(blk + (size_t)g * 2048 + 1024 * h + 16 * l,
+                       q + (size_t)(rb * 16 + l % 16) * K + 128 * g + 64 * h + 16 * (l / 16), 16);
+    uint8_t* dst = blk + (size_t)16 * K;
+    memset(dst, 0, rowblock_bytes(K, MOE_FP8_B128) - (size_t)16 * K);
+    memcpy(dst, sc + (size_t)(rb / 8) * G, (size_t)G * 4);
+}
+
 moe_status moe_pack_expert(moe_dtype w, int d, int f, const void* wg, const void* wu, const void* wd,
                            const void* sg, const void* su, const void* sd, void* slot_out) {
     MOE_CHECK(slot_shape_ok(d, f, w), MOE_ESHAPE, "moe_pack_expert: unsupported shape d=%d f=%d dtype=%d", d,
               f, (int)w);
     MOE_CHECK(wg && wu && wd && slot_out, MOE_EINVAL, "moe_pack_expert: NULL weight or output");
-    const bool i4 = w == MOE_INT4_G128;
-    if (i4) MOE_CHECK(sg && su && sd, MOE_EINVAL, "moe_pack_expert: int4 needs scales");
-    else MOE_CHECK(!sg && !su && !sd, MOE_EINVAL, "moe_pack_expert: scales only for int4");
+    const bool i4 = w == MOE_INT4_G128, f8 = w == MOE_FP8_B128;
+    if (i4 || f8) MOE_CHECK(sg && su && sd, MOE_EINVAL, "moe_pack_expert: int4 and fp8 need scales");
+    else MOE_CHECK(!sg && !su && !sd, MOE_EINVAL, "moe_pack_expert: scales only for int4 and fp8");
     uint8_t* out = (uint8_t*)slot_out;
     size_t total = moe_slot_bytes(d, f, w);
     memset(out + slot_bytes_raw(d, f, w), 0, total - slot_bytes_raw(d, f, w));
@@ -178,11 +192,13 @@ moe_status moe_pack_expert(moe_dtype w, int d, int f, const void* wg, const void
             const void* m = which ? wu : wg;
             uint8_t* blk = out + gu_block_offset(b, which, d, w);
             if (i4) pack_int4_block((const uint8_t*)m, (const uint16_t*)(which ? su : sg), b, d, blk);
+            else if (f8) pack_fp8_block((const uint8_t*)m, (const float*)(which ? su : sg), b, d, blk);
             else pack_dense_block((const uint8_t*)m, b, d, esz, blk);
         } else {
             int b = i - 2 * ngu;
             uint8_t* blk = out + down_block_offset(b, d, f, w);
             if (i4) pack_int4_block((const uint8_t*)wd, (const uint16_t*)sd, b, f, blk);
+            else if (f8) pack_fp8_block((const uint8_t*)wd, (const float*)sd, b, f, blk);
             else pack_dense_block((const uint8_t*)wd, b, f, esz, blk);
         }
     });

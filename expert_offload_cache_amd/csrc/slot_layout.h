@@ -10,12 +10,13 @@
 
 namespace moe {
 
-// bytes of one 16-row block of a [R, K] matrix (fragments, then int4 scales)
+// bytes of one 16-row block of a [R, K] matrix (fragments, then int4 or fp8 scales)
 __host__ __device__ inline size_t rowblock_bytes(int K, moe_dtype w) {
     switch (w) {
         case MOE_F32: return (size_t)16 * K * 4;
         case MOE_BF16: return (size_t)16 * K * 2;
         case MOE_INT4_G128: return (size_t)8 * K + (size_t)32 * (K / 128);
+        case MOE_FP8_B128: return (size_t)16 * K + ((size_t)4 * (K / 128) + 63) / 64 * 64;
     }
     return 0;
 }
@@ -31,8 +32,8 @@ __host__ __device__ inline size_t down_block_offset(int b, int d, int f, moe_dty
 }
 
 inline bool slot_shape_ok(int d, int f, moe_dtype w) {
-    int q = (w == MOE_INT4_G128) ? 128 : 32;
-    if (w != MOE_F32 && w != MOE_BF16 && w != MOE_INT4_G128) return false;
+    int q = (w == MOE_INT4_G128 || w == MOE_FP8_B128) ? 128 : 32;
+    if (w != MOE_F32 && w != MOE_BF16 && w != MOE_INT4_G128 && w != MOE_FP8_B128) return false;
     return d >= 64 && f >= 64 && d <= 16384 && f <= 16384 && d % q == 0 && f % q == 0;
 }
 

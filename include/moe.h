@@ -31,7 +31,15 @@
  *   - DETERMINISM: identical inputs give bitwise identical outputs; no atomics
  *     decide positions or the order of any floating-point sum.
  *   - DTYPES: activations MOE_F32 or MOE_BF16 (bfloat16 bit patterns, uint16);
- *     weights MOE_F32, MOE_BF16 or MOE_INT4_G128.
+ *     weights MOE_F32, MOE_BF16, MOE_INT4_G128 or MOE_FP8_B128.
+ *   - FP8: e4m3 values (4 exponent bits, 3 mantissa bits, largest finite value 448, NaN, no
+ *     infinity) with binary32 scales: activation rows one per row and 128 consecutive columns,
+ *     weights one per 128 x 128 block.  Rows are quantised group by group: m = the largest
+ *     magnitude, s = max(m / 448, 2^-126), q = e4m3(v * (1 / s)), where m / 448, 1 / s and the
+ *     product are each rounded once to binary32 and the result to the nearest e4m3, ties to even.
+ *     A group that holds a NaN or an infinity reads back as NaN in every place.  The quotient is
+ *     not rounded to a power of two; such scales, where a checkpoint has them, are binary32
+ *     numbers like any others.
  */
 #ifndef MOE_H_
 #define MOE_H_
@@ -60,7 +68,7 @@ enum {
 /* element type codes (an integer, so that any value a caller passes is well defined; values other
  * than these are rejected with MOE_EDTYPE) */
 typedef int32_t moe_dtype;
-enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_INT4_G128 = 2 };
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_INT4_G128 = 2, MOE_FP8_B128 = 3 };
 typedef void* moe_stream;
 
 MOE_API const char* moe_last_error(void);
@@ -83,16 +91,22 @@ MOE_API const char* moe_version(void);
  *     offset 16*l: row l%16, word s (0..3) holds inputs 32s + 8*(l/16) + (0..7); input pair
  *     (2p, 2p+1) of a word sits in bits [4p, 4p+4) and [16+4p, 20+4p).  A stored nibble u is
  *     the integer u - 8 in [-7, 7]; weight = (u - 8) * scale of its row and 128-group.
+ *   FP8_B128: a 16-row block is K/128 fragments of 16 rows x 128 inputs (2048 bytes), then K/128
+ *     binary32 scales (those of the 128 x 128 blocks that hold the 16 rows), zero-padded to a multiple
+ *     of 64 bytes.  A fragment is two halves of 1024 bytes, inputs 0..63 and 64..127; in a half
+ *     lane l owns 16 bytes at offset 16*l: row l%16, inputs 16*(l/16) .. 16*(l/16)+15 of the half.
  * ------------------------------------------------------------------------------------------ */
 
 /* Bytes of one packed expert (a multiple of 256).  0 if the shape/dtype is unsupported:
- * d, f multiples of 32 (F32/BF16) or of 128 (INT4_G128), 64 <= d, f <= 16384. */
+ * d, f multiples of 32 (F32/BF16) or of 128 (INT4_G128, FP8_B128), 64 <= d, f <= 16384. */
 MOE_API size_t moe_slot_bytes(int d, int f, moe_dtype w);
 
 /* Pack one expert from the canonical row-major layout into a slot image (host memory).
  * F32/BF16: wg, wu [f][d], wd [d][f] in the weight dtype; sg, su, sd must be NULL.
  * INT4_G128: wg, wu [f][d/2], wd [d][f/2] bytes (element 2i low nibble of byte i, offset
- * binary); sg, su [f][d/128], sd [d][f/128] bf16 scale bits.  slot_out: moe_slot_bytes bytes. */
+ * binary); sg, su [f][d/128], sd [d][f/128] bf16 scale bits.
+ * FP8_B128: wg, wu [f][d], wd [d][f] e4m3 bytes; sg, su [f/128][d/128], sd [d/128][f/128] binary32.
+ * slot_out: moe_slot_bytes bytes. */
 MOE_API moe_status moe_pack_expert(moe_dtype w, int d, int f, const void* wg, const void* wu,
                                    const void* wd, const void* sg, const void* su, const void* sd,
                                    void* slot_out);
@@ -172,7 +186,10 @@ MOE_API moe_status moe_route_permute(const void* x, moe_dtype act, int T, int d,
  *   intermediate rows may be bf16 like h.  Any other value: MOE_EDTYPE.
  *   ws: device workspace of at least moe_workspace_bytes(...) bytes, zero-filled before its
  *   first use.  Its first 4 bytes are a sticky int32 status word (0 = no error).
- * Intermediate h is rounded to bf16 when act is BF16 (binary32 when act is F32). */
+ * Intermediate h is rounded to bf16 when act is BF16 (binary32 when act is F32).
+ * Weights FP8_B128 need act BF16: each row of x is quantised (see FP8 above), the gate and up sums
+ * are of 8-bit products, h is quantised from its binary32 values and the down projection's products
+ * are of 8-bit values again: bitwise what moe_quant_fp8 and moe_expert_ffn_fp8 give. */
 #define MOE_SLOT_ELSEWHERE (-2)
 /* Above 64 tokens (prefill) the experts run on the matrix-core grouped GEMM, which feeds int4
  * weights to the matrix cores as bf16(q * s).  Experts holding at most moe_prefill_gemv_tokens(w)
@@ -188,6 +205,16 @@ MOE_API moe_status moe_expert_ffn_grouped(const void* x, moe_dtype act, int T, i
                                           int n_slots, const void* slot_pool, size_t slot_stride,
                                           moe_dtype w, const void* shared_w, void* y_perm,
                                           moe_dtype y_dtype, void* ws, size_t ws_bytes, moe_stream s);
+
+/* moe_expert_ffn_grouped with FP8_B128 weights for rows that are already quantised (by moe_add_rmsnorm
+ * or moe_quant_fp8): x e4m3 [T,d] (rows back to back, 16-byte aligned), x_scale binary32 [T, d/128].
+ * y_dtype F32 or BF16.  ws: moe_workspace_bytes(T, d, f, E, k, has_shared, MOE_BF16, MOE_FP8_B128)
+ * bytes.  Everything else as moe_expert_ffn_grouped. */
+MOE_API moe_status moe_expert_ffn_fp8(const void* x, const float* x_scale, int T, int d, int f, int E, int k,
+                                      const int32_t* perm, const int32_t* offsets, const int32_t* counts,
+                                      const int32_t* slot_of_expert, int n_slots, const void* slot_pool,
+                                      size_t slot_stride, const void* shared_w, void* y_perm, moe_dtype y_dtype,
+                                      void* ws, size_t ws_bytes, moe_stream s);
 
 /* moe_expert_ffn_grouped for callers that cannot allocate device memory (code under HIP graph
  * capture, tight serving loops, harnesses that forbid hipMalloc): the same kernels, with the
@@ -216,6 +243,43 @@ MOE_API moe_status moe_expert_ffn_grouped_noalloc(const void* x, moe_dtype act, 
 MOE_API moe_status moe_combine(const void* y_perm, moe_dtype y_dtype, const float* topk_w,
                                const int32_t* inv_perm, int T, int k, int d, int has_shared, void* y,
                                moe_dtype out, moe_stream s);
+
+/* ------------------------------------------------------------------------------------------
+ * moe_add_rmsnorm -- the norm that stands before a layer, with the residual's addition (the pages
+ * describe the layer from its input on; plain reading):
+ *   h = x + residual, rounded to act (resid_out; without a residual h = x and resid_out is NULL),
+ *   y = h / sqrt(mean(h^2) + eps) * weight, squares, mean and quotient in binary32,
+ * of the rounded h: what the addition and the norm give one after the other.
+ *   x, residual, resid_out [T,d] act, y [T,d] act or NULL, q [T,d] e4m3 with scale [T, ceil(d/128)]
+ *   (both or neither), quantised from y before its rounding to act; at least one of y and q.
+ *   weight [d] act or F32 (w_dtype).  ldx, ldr, ldro, ldy, ldq: elements from a row to the next,
+ *   at least d (ignored for NULL pointers).
+ * Rows: each is read once; one whose h^2 overflow binary32 gives zeros, one with a NaN or an infinity
+ * NaN.  The result of a row does not depend on T.  resid_out may be x or residual, y may be x or
+ * residual (same stride); no other overlap.  Any d from 1 to 16384 and any alignment to the
+ * element; rows on 16 bytes (q on 8) with d a multiple of 8 are faster. */
+MOE_API moe_status moe_add_rmsnorm(const void* x, moe_dtype act, int T, int d, size_t ldx, const void* residual,
+                                   size_t ldr, const void* weight, moe_dtype w_dtype, float eps, void* resid_out,
+                                   size_t ldro, void* y, size_t ldy, void* q, size_t ldq, float* scale,
+                                   moe_stream s);
+
+/* moe_quant_fp8 -- activation rows x [T,d] act into e4m3 rows q and their scales [T, ceil(d/128)]
+ * (see FP8 above; the last group of a row may be shorter).  Strides, widths and alignment as in
+ * moe_add_rmsnorm. */
+MOE_API moe_status moe_quant_fp8(const void* x, moe_dtype act, int T, int d, size_t ldx, void* q, size_t ldq,
+                                 float* scale, moe_stream s);
+
+/* moe_gemm_fp8 -- the product of quantised rows and a quantised matrix (a layer's projections next
+ * to its experts):
+ *   c[m,n] = sum_g a_scale[m,g] * w_scale[n/128,g] * sum_{k in group g} a[m,k] * w[n,k],
+ * products of e4m3 values and their sums in binary32, each c rounded once to out (F32 or BF16).
+ *   a [M,K] e4m3, a_scale [M, ceil(K/128)]; w [N,K] e4m3 (rows are outputs), w_scale
+ *   [ceil(N/128), ceil(K/128)]; c [M,N].  lda, ldw, ldc: elements from a row to the next.
+ * K a multiple of 16 (the last group may be shorter); rows of a and w start on 16 bytes; M and N
+ * are free.  c overlaps none of the inputs. */
+MOE_API moe_status moe_gemm_fp8(const void* a, size_t lda, const float* a_scale, int M, int K, const void* w,
+                                size_t ldw, const float* w_scale, int N, void* c, size_t ldc, moe_dtype out,
+                                moe_stream s);
 
 /* ------------------------------------------------------------------------------------------
  * Expert-slot cache shared by all MoE layers (FreeToken linux guide, "MoE memory handling":

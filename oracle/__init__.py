@@ -12,6 +12,7 @@ arithmetic; the layer form below is the plain reading, stated per function):
 * route     -- router logits, top-k, renormalised softmax gates   (``route.py``)
 * permute   -- tokens grouped by expert, stable within an expert  (``permute.py``)
 * expert    -- SwiGLU expert FFN, float64, from exactly decoded weights (``ffn.py``)
+* fp8       -- e4m3 rows and matrices with block scales, the norm, the quantised expert (``fp8.py``)
 * layer     -- gate-weighted combine (+ always-on shared expert)  (``layer.py``)
 * lru       -- the slot cache shared by all layers: LRU simulator,
                brute-force LRU and a stack-distance recomputation (``lru.py``)

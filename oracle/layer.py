@@ -17,6 +17,7 @@ from __future__ import annotations
 import numpy as np
 
 from .ffn import swiglu_expert
+from .fp8 import swiglu_expert_fp8
 from .numerics import act_to_f64, expert_to_f64
 from .permute import permute
 from .router import route
@@ -26,6 +27,11 @@ def layer_from_inputs(li):
     """synth.LayerInputs -> dict of the arrays the oracle needs (weights decoded lazily)."""
     return dict(x=li.x, w_router=li.w_router, bias=li.bias, act=li.wl.act, k=li.wl.k, E=li.wl.E,
                 experts=li.experts, shared=li.shared)
+
+
+def _expert_form(ew):
+    """Experts with 8-bit weights take quantised rows."""
+    return swiglu_expert_fp8 if getattr(ew, "wdt", None) == "fp8" else swiglu_expert
 
 
 def _expert_cache(experts):
@@ -56,10 +62,10 @@ def moe_layer(x, w_router, bias, act, k, E, experts, shared=None, forced_idx=Non
             if hi == lo:
                 continue
             flat = perm[lo:hi]
-            y_pairs[flat] = swiglu_expert(xf[flat // k], *get(e))
+            y_pairs[flat] = _expert_form(experts[e])(xf[flat // k], *get(e))
         y = (gates[:, :, None] * y_pairs.reshape(T, k, d)).sum(axis=1)
         if shared is not None:
-            y = y + swiglu_expert(xf, *expert_to_f64(shared))
+            y = y + _expert_form(shared)(xf, *expert_to_f64(shared))
     return dict(y=y, logits=logits, topk_idx=idx, gates=gates, counts=counts, offsets=offsets,
                 perm=perm, inv_perm=inv)
 
@@ -96,7 +102,8 @@ def moe_layer_tokens(tokens, x, w_router, bias, act, k, E, experts, shared=None,
     with np.errstate(over="ignore"):
         for t in range(n):
             for j in range(k):
-                y[t] += gates[t, j] * swiglu_expert(xf[t:t + 1], *get(int(idx[t, j])))[0]
+                e = int(idx[t, j])
+                y[t] += gates[t, j] * _expert_form(experts[e])(xf[t:t + 1], *get(e))[0]
         if shared is not None:
-            y = y + swiglu_expert(xf, *expert_to_f64(shared))
+            y = y + _expert_form(shared)(xf, *expert_to_f64(shared))
     return dict(y=y, logits=logits, topk_idx=idx, gates=gates)

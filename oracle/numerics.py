@@ -8,6 +8,8 @@ high nibble.  q * s is exact in binary64 (and in binary32).
 """
 import numpy as np
 
+from . import fp8
+
 
 def bf16_to_f32(bits: np.ndarray) -> np.ndarray:
     return (np.asarray(bits, dtype=np.uint16).astype(np.uint32) << np.uint32(16)).view(np.float32)
@@ -49,6 +51,8 @@ def expert_to_f64(ew, int4_bf16: bool = False):
     if ew.wdt == "int4":
         return (dequant_int4(ew.wg, ew.sg, int4_bf16), dequant_int4(ew.wu, ew.su, int4_bf16),
                 dequant_int4(ew.wd, ew.sd, int4_bf16))
+    if ew.wdt == "fp8":
+        return fp8.matrix_value(ew.wg, ew.sg), fp8.matrix_value(ew.wu, ew.su), fp8.matrix_value(ew.wd, ew.sd)
     if ew.wdt == "bf16":
         return bf16_to_f64(ew.wg), bf16_to_f64(ew.wu), bf16_to_f64(ew.wd)
     return (np.asarray(ew.wg, np.float64), np.asarray(ew.wu, np.float64), np.asarray(ew.wd, np.float64))

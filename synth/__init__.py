@@ -1,7 +1,7 @@
 """Seeded synthetic inputs for the routed-expert MoE layer.
 
 This module produces inputs only: activations, router weights and bias,
-expert weights (bf16, fp32, or int4 with bf16 group scales), slot orders and
+expert weights (bf16, fp32, int4 with bf16 group scales, or e4m3 with block scales), slot orders and
 routing traces.  It computes no step of the layer itself, and both the oracle
 and the HIP path read their inputs from here.
 
@@ -111,6 +111,35 @@ def quant_int4(seed: int, stream: int, rows: int, K: int, sigma: float, w: Optio
     return packed, scales
 
 
+# the 127 finite e4m3 magnitudes by code: subnormal steps of 2^-9, then 8 steps a binade up to 448
+_E4M3 = np.array([m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10) for e in range(16) for m in range(8)][:127])
+
+
+def e4m3_bits(v: np.ndarray) -> np.ndarray:
+    """e4m3 bit patterns (uint8) of float64 values of magnitude below 464, nearest, ties to the even code."""
+    a = np.abs(np.asarray(v, dtype=np.float64))
+    lo = np.clip(np.searchsorted(_E4M3, a, side="right") - 1, 0, 125)
+    mid = (_E4M3[lo] + _E4M3[lo + 1]) / 2
+    up = (a > mid) | ((a == mid) & (lo % 2 == 1))
+    return ((lo + up).astype(np.uint8) | (np.signbit(v).astype(np.uint8) << 7)).astype(np.uint8)
+
+
+def quant_fp8(seed: int, stream: int, rows: int, K: int, sigma: float, w: Optional[np.ndarray] = None):
+    """e4m3 bit patterns [rows, K] with one float32 scale per 128 x 128 block, [ceil(rows/128), ceil(K/128)]:
+    scale = the block's largest magnitude / 448 (at least 2^-126), value = e4m3(w / scale).  The float matrix
+    is generated from (seed, stream, sigma) unless ``w`` is given."""
+    w = normal_f32(seed, stream, (rows, K), sigma) if w is None else np.asarray(w, dtype=np.float32)
+    bits = np.empty((rows, K), dtype=np.uint8)
+    scales = np.empty(((rows + 127) // 128, (K + 127) // 128), dtype=np.float32)
+    for i in range(scales.shape[0]):
+        for j in range(scales.shape[1]):
+            blk = w[128 * i:128 * i + 128, 128 * j:128 * j + 128].astype(np.float64)
+            s = np.float32(max(np.abs(blk).max() / 448.0, 2.0 ** -126))
+            scales[i, j] = s
+            bits[128 * i:128 * i + 128, 128 * j:128 * j + 128] = e4m3_bits(blk / np.float64(s))
+    return bits, scales
+
+
 # ----------------------------------------------------------------------------------------------
 # workloads
 # ----------------------------------------------------------------------------------------------
@@ -124,7 +153,7 @@ class Workload:
     k: int
     f: int
     act: str  # "f32" | "bf16"
-    wdt: str  # "f32" | "bf16" | "int4"
+    wdt: str  # "f32" | "bf16" | "int4" | "fp8"
     T_list: tuple
     shared: bool = False
     zipf_bias: Optional[float] = None  # Zipf exponent s of the router bias, None = no bias
@@ -181,6 +210,7 @@ class ExpertWeights:
     dense dtypes: wg, wu [f, d], wd [d, f] as float32 or bf16 bits (uint16).
     int4: wg, wu, wd are packed nibbles [rows, K//2] and sg, su, sd their
     bf16 scales [rows, K//128].
+    fp8: e4m3 bytes [f, d] / [d, f], and sg, su, sd float32 scales per 128 x 128 block.
     """
 
     wdt: str
@@ -202,6 +232,11 @@ def expert_weights(wl: Workload, seed: int, layer: int, expert: int, shared: boo
         pu, su = quant_int4(seed, su_, f, d, s)
         pd, sd = quant_int4(seed, sd_, d, f, s)
         return ExpertWeights("int4", pg, pu, pd, sg, su, sd)
+    if wl.wdt == "fp8":
+        pg, sg = quant_fp8(seed, sg_, f, d, s)
+        pu, su = quant_fp8(seed, su_, f, d, s)
+        pd, sd = quant_fp8(seed, sd_, d, f, s)
+        return ExpertWeights("fp8", pg, pu, pd, sg, su, sd)
     return ExpertWeights(wl.wdt, _dense(seed, sg_, (f, d), s, wl.wdt), _dense(seed, su_, (f, d), s, wl.wdt),
                          _dense(seed, sd_, (d, f), s, wl.wdt))
 

@@ -1,0 +1,508 @@
+"""The 8-bit operators on the GPU against their definitions in 64 bits (oracle/fp8.py).
+
+Tolerances, u = 2^-24 (half a binary32 step):
+- quantisation of given rows: bitwise (the definition fixes every rounding).
+- norm in binary32: the sum of squares adds positive terms, at most 16 in a lane, 6 levels of lanes and
+  16 waves, so 38 u, halved by the square root, and 6 more roundings (mean, eps, root, quotient, two
+  products): 25 u, taken as 32 u of the value.  bf16 rows: 2^-8 more.  q of the norm: the value may move by 32 u
+  and the scale by 32 u before it is rounded, so q lies between the roundings of v/s (1 -+ 2^-18).
+- product: each of K products and G group terms is added with a rounding of at most u of the sum of
+  magnitudes M = sum |a w| s s': (K + 4 G) u M.  The e4m3 instructions drop what falls below 18 bits of
+  the largest product of a group: 2^-18 of it for each of the 128.
+- experts: h differs by some 2^-17 relative, an element lies that near to a border of two e4m3 values with a
+  chance of 32 * 2^-17 and then moves by at most 1/8: sqrt(2^-12) / 8 = 2e-3 of a row in the mean.  Rows are held
+  to 2e-2 (the bound of the bf16 and int4 layers), their mean to 5e-3.
+"""
+import gc
+
+import numpy as np
+import pytest
+
+import synth
+from gpu_util import need_gpu, rel_err_per_token, small_workload, to_dev, y_to_f64
+from oracle import fp8
+from oracle.layer import moe_layer
+from oracle.numerics import expert_to_f64
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def moe():
+    need_gpu()
+    import expert_offload_cache_amd as m
+
+    return m
+
+
+def _bits(t):
+    import torch
+
+    view = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]
+    return t.contiguous().view(view).cpu().numpy()
+
+
+def _rows(rng, T, d, dtype):
+    import torch
+
+    v = rng.normal(size=(T, d)).astype(np.float32)
+    v[:, rng.integers(0, d, max(1, d // 100))] *= 12
+    return torch.from_numpy(v).cuda().to(dtype)
+
+
+def _check_quant(x, q, s):
+    want_q, want_s = fp8.quantise(x.float().cpu().numpy())
+    assert np.array_equal(s.cpu().numpy().astype(np.float64), want_s, equal_nan=True)
+    assert np.array_equal(fp8.decode(_bits(q)), want_q, equal_nan=True)
+
+
+# ---- rows -------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1, 1), (1, 128), (3, 7), (5, 129), (2, 512), (7, 520), (9, 1024), (33, 1032), (4, 2000),
+                                 (130, 2048), (3, 4096), (2, 4104), (3, 8192), (2, 16384), (1, 16383)])
+def test_quant_rows(moe, T, d, dt):
+    import torch
+
+    x = _rows(np.random.default_rng([T, d]), T, d, torch.bfloat16 if dt == "bf16" else torch.float32)
+    q, s = moe.quant_fp8(x)
+    _check_quant(x, q, s)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_quant_special_values(moe, dt):
+    """Zeros, subnormals, the type's largest, ties, infinities and NaN: their group alone is affected."""
+    import torch
+
+    x = torch.zeros(8, 256, dtype=torch.float32)
+    x[1] = torch.linspace(-1, 1, 256) * 2.0 ** -130
+    x[2] = torch.linspace(-1, 1, 256) * 3.0e38
+    x[3, :4] = torch.tensor([7.0, -7.0, 6.75, 3.625])
+    x[4, 5], x[4, 200] = float("inf"), 1.0
+    x[5, 7], x[5, 130] = float("nan"), 2.0
+    x[6, 0], x[6, 1] = -float("inf"), float("nan")
+    x[7] = torch.arange(256) * 2.0 ** -9
+    x = x.cuda().to(torch.bfloat16 if dt == "bf16" else torch.float32)
+    q, s = moe.quant_fp8(x)
+    v = fp8.rows_value(fp8.decode(_bits(q)), s.cpu().numpy().astype(np.float64))
+    # a group's only value is 448 s, and s = fl32(m / 448) is within half a step, u relative, of m / 448
+    assert np.isnan(v[4, :128]).all() and abs(v[4, 200] - 1.0) <= U
+    assert np.isnan(v[5, :128]).all() and abs(v[5, 130] - 2.0) <= 2 * U
+    assert np.isnan(v[6, :128]).all() and not v[6, 128:].any()
+    ok = [0, 1, 2, 3, 7]
+    _check_quant(x[ok], q[ok], s[ok])
+
+
+@pytest.mark.parametrize("T,d,ld,off", [(5, 256, 264, 0), (5, 256, 257, 1), (4, 100, 333, 3), (65, 1024, 1040, 8)])
+def test_rows_with_strides_and_any_alignment(moe, T, d, ld, off):
+    import torch
+
+    for dt in (torch.bfloat16, torch.float32):
+        big = _rows(np.random.default_rng(1), T, ld + off, dt)
+        x = big[:, off:off + d]
+        qb = torch.full((T, ld + off), 0x11, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        s = torch.empty(T, -(-d // 128), device="cuda")
+        q, _ = moe.quant_fp8(x, out=(qb[:, off:off + d], s))
+        _check_quant(x, q, s)
+        rest = np.ones(ld + off, bool)
+        rest[off:off + d] = False
+        assert (_bits(qb)[:, rest] == 0x11).all()
+        w = _rows(np.random.default_rng(2), 1, d + 1, dt)[0, 1:].clone()
+        y, _, _, _ = moe.add_rmsnorm(x, w)
+        _check_norm(x, None, w, 1e-6, y, None, None, None)
+
+
+def _check_norm(x, r, w, eps, y, h, q, s):
+    import torch
+
+    bf16 = x.dtype == torch.bfloat16
+    x64, w64 = x.double().cpu().numpy(), w.double().cpu().numpy()
+
+    def round_sum(v):
+        return torch.from_numpy(v.astype(np.float32)).to(x.dtype).double().numpy()
+
+    h_ref, y_ref = fp8.add_rmsnorm(x64, None if r is None else r.double().cpu().numpy(), w64, eps, round_sum)
+    if r is not None:
+        assert np.array_equal(h.double().cpu().numpy(), h_ref)
+    if y is not None:
+        err = np.abs(y.double().cpu().numpy() - y_ref)
+        assert (err <= ((2.0 ** -8 if bf16 else 0) + 32 * U) * np.abs(y_ref) + 2.0 ** -126).all()
+    if q is not None:
+        s64 = s.cpu().numpy().astype(np.float64)
+        _, s_ref = fp8.quantise(y_ref)
+        assert (np.abs(s64 - s_ref) <= 34 * U * s_ref).all()
+        v = np.abs(y_ref) / np.repeat(s64, 128, axis=1)[:, :y_ref.shape[1]]
+        qv = fp8.decode(_bits(q))
+        assert ((np.sign(qv) == np.sign(y_ref)) | (qv == 0)).all()
+        lo, hi = fp8.round_e4m3(v * (1 - 2.0 ** -18)), fp8.round_e4m3(np.minimum(v * (1 + 2.0 ** -18), 463))
+        assert ((np.abs(qv) >= lo) & (np.abs(qv) <= hi)).all()
+
+
+@pytest.mark.parametrize("emit", ["y", "fp8", "both"])
+@pytest.mark.parametrize("act,wt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("T,d,res", [(1, 64, True), (3, 130, True), (17, 512, False), (6, 1000, True), (2, 2048, False),
+                                     (5, 4096, True), (3, 7168, True), (2, 16384, True), (1, 5, False)])
+def test_add_rmsnorm(moe, T, d, res, act, wt, emit):
+    import torch
+
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}
+    rng = np.random.default_rng([T, d])
+    x, w = _rows(rng, T, d, dt[act]), (1 + 0.2 * _rows(rng, 1, d, torch.float32)[0]).to(dt[wt])
+    r = _rows(rng, T, d, dt[act]) if res else None
+    y, h, q, s = moe.add_rmsnorm(x, w, 1e-5, residual=r, emit=emit)
+    assert (y is None) == (emit == "fp8") and (q is None) == (emit == "y") and (h is None) == (not res)
+    _check_norm(x, r, w, 1e-5, y, h, q, s)
+
+
+def test_norm_in_place_and_row_independence(moe):
+    """The sum may overwrite the residual and y the rows; a row's bits do not depend on the others;
+    a row of zeros, of infinities or with a NaN affects itself alone."""
+    import torch
+
+    rng = np.random.default_rng(5)
+    T, d = 37, 2048
+    x, r = _rows(rng, T, d, torch.bfloat16), _rows(rng, T, d, torch.bfloat16)
+    w = (1 + 0.2 * _rows(rng, 1, d, torch.float32)[0]).to(torch.bfloat16)
+    x[3], r[3], x[4, 9], x[5, 0] = 0, 0, float("nan"), float("inf")
+    y, h, q, s = moe.add_rmsnorm(x, w, residual=r, emit="both")
+    one = [moe.add_rmsnorm(x[i:i + 1], w, residual=r[i:i + 1], emit="both") for i in range(T)]
+    for k, t in enumerate((y, h, q, s)):
+        assert np.array_equal(_bits(t), np.concatenate([_bits(o[k]) for o in one]))
+    assert not y[3].any() and torch.isnan(y[4]).all() and torch.isnan(y[5, 0])
+    rows = [i for i in range(T) if i not in (3, 4, 5)]
+    _check_norm(x[rows], r[rows], w, 1e-6, y[rows], h[rows], q[rows], s[rows])
+    x2, r2 = x.clone(), r.clone()
+    moe.add_rmsnorm(x2, w, residual=r2, emit="both", out=(x2, r2, torch.empty_like(q), torch.empty_like(s)))
+    assert np.array_equal(_bits(x2), _bits(y)) and np.array_equal(_bits(r2), _bits(h))
+
+
+# ---- the dense product ------------------------------------------------------------------------------
+def _operands(rng, M, N, K, lda=None, ldw=None):
+    """Quantised operands; columns past K of a wider row hold NaN codes."""
+    import torch
+
+    def mat(rows, ld, vals):
+        full = np.full((rows, ld or K), 0x7F, np.uint8)
+        full[:, :K] = synth.e4m3_bits(np.clip(vals, -448, 448))
+        return full, torch.from_numpy(full).cuda().view(torch.float8_e4m3fn)[:, :K]
+
+    G = -(-K // 128)
+    a, at = mat(M, lda, rng.normal(size=(M, K)) * 100)
+    w, wt = mat(N, ldw, rng.normal(size=(N, K)) * 100)
+    sa = rng.uniform(0.5, 2, size=(M, G)).astype(np.float32) / 100
+    sw = rng.uniform(0.5, 2, size=(-(-N // 128), G)).astype(np.float32) / 5000
+    return (a[:, :K], sa, w[:, :K], sw), (at, torch.from_numpy(sa).cuda(), wt, torch.from_numpy(sw).cuda())
+
+
+def _check_product(ops, c, fast):
+    a, sa, w, sw = ops
+    A, W = fp8.rows_value(fp8.decode(a), sa.astype(np.float64)), fp8.matrix_value(w, sw)
+    ref, mag = A @ W.T, np.abs(A) @ np.abs(W).T
+    K, G = a.shape[1], sa.shape[1]
+    tol = (K + 4 * G) * U * mag
+    if c.dtype.itemsize == 2:
+        tol = tol + 2.0 ** -8 * np.abs(ref)
+    if fast:  # 2^-18 of a group's largest product, at most 448^2 times the scales, for each of its 128
+        swr = np.repeat(sw, 128, axis=0)[:w.shape[0]].astype(np.float64)
+        tol = tol + 128 * 2.0 ** -18 * 448 ** 2 * (sa.astype(np.float64) @ swr.T)
+    err = np.abs(y_to_f64(c) - ref)
+    assert (err <= tol).all(), (err / tol).max()
+    return ref
+
+
+SHAPES = [(1, 1, 16), (1, 128, 128), (1, 2048, 4096), (2, 100, 48), (3, 17, 2000), (16, 130, 256), (17, 64, 144),
+          (31, 257, 1040), (33, 16, 128), (64, 512, 768), (65, 96, 384), (100, 1001, 272), (128, 640, 1024),
+          (129, 48, 16), (200, 515, 2064), (300, 1024, 512), (513, 770, 1296)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(moe, M, N, K, out):
+    import torch
+
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    ops, dev = _operands(np.random.default_rng([M, N, K]), M, N, K)
+    c = moe.gemm_fp8(*dev, out_dtype=dt)
+    assert c.dtype == dt
+    _check_product(ops, c, fast=out == "bf16")
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 150, 700])
+def test_product_strides(moe, M):
+    """Wider rows (their rest NaN), a result inside a wider matrix at an odd element, and nothing written
+    beside it or in the rows behind."""
+    import torch
+
+    N, K = 131, 208
+    ops, dev = _operands(np.random.default_rng(M), M, N, K, lda=K + 32, ldw=K + 16)
+    for dt in (torch.bfloat16, torch.float32):
+        big = torch.full((M + 2, N + 6), -7.0, dtype=dt, device="cuda")
+        moe.gemm_fp8(*dev, out=big[:M, 3:3 + N])
+        _check_product(ops, big[:M, 3:3 + N].contiguous(), fast=dt == torch.bfloat16)
+        rest = torch.ones_like(big, dtype=torch.bool)
+        rest[:M, 3:3 + N] = False
+        assert (big[rest] == -7.0).all()
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_product_nan_and_infinite_scales(moe, M):
+    """A NaN in a row or a matrix row reaches that row or column alone; so does an infinite scale."""
+    import torch
+
+    N, K = 256, 384
+    _, (a, sa, w, sw) = _operands(np.random.default_rng(M), M, N, K)
+    ref = moe.gemm_fp8(a, sa, w, sw, out_dtype=torch.float32)
+    w2, sa2 = w.clone(), sa.clone()
+    w2.view(torch.uint8)[7, 100] = 0x7F
+    w2.view(torch.uint8)[200, 383] = 0xFF
+    sa2[M - 1, 1] = float("inf")
+    c = moe.gemm_fp8(a, sa2, w2, sw, out_dtype=torch.float32)
+    cols = torch.ones(N, dtype=torch.bool, device="cuda")
+    cols[[7, 200]] = False
+    assert torch.isnan(c[:, ~cols]).all() and not torch.isfinite(c[M - 1]).any()
+    assert torch.equal(c[:M - 1, cols], ref[:M - 1, cols])
+    assert moe.gemm_fp8(a[:0], sa[:0], w, sw).shape == (0, N)
+
+
+def test_product_repeats_bitwise_on_another_stream(moe):
+    import torch
+
+    for M, N, K in ((1, 512, 1024), (48, 512, 1024), (700, 512, 1024)):
+        _, dev = _operands(np.random.default_rng(0), M, N, K)
+        first = moe.gemm_fp8(*dev)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        outs = [moe.gemm_fp8(*dev, stream=side, out=torch.empty_like(first)) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(first, o) for o in outs)
+
+
+# ---- the experts ------------------------------------------------------------------------------------
+CASES = [(dict(d=256, f=128, E=8, k=2, shared=True), 1), (dict(d=256, f=128, E=8, k=2, shared=True), 40),
+         (dict(d=384, f=640, E=5, k=5), 3), (dict(d=128, f=128, E=1, k=1), 70), (dict(d=512, f=384, E=300, k=7), 33),
+         (dict(d=640, f=256, E=16, k=4, shared=True), 64), (dict(d=256, f=256, E=6, k=2, shared=True), 65),
+         (dict(d=512, f=384, E=12, k=3), 333), (dict(d=768, f=128, E=4, k=2, shared=True), 700)]
+
+
+@pytest.mark.parametrize("shape,T", CASES, ids=[f"{c[0]['d']}x{c[0]['f']}x{c[0]['E']}_T{c[1]}" for c in CASES])
+def test_layer_with_fp8_experts(moe, shape, T):
+    """The layer against the oracle; e4m3 rows give the bits that bf16 rows give; a second call repeats."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    wl = small_workload("bf16", "fp8", shape["d"], shape["f"], shape["E"], shape["k"], shared=shape.get("shared", False))
+    li = synth.layer_inputs(wl, T, seed=1)
+    layer = DeviceLayer.from_inputs(li)
+    x = layer.x_to_device(li.x)
+    out = layer.forward(x)
+    ref = moe_layer(li.x, li.w_router, li.bias, "bf16", wl.k, wl.E, li.experts, li.shared)
+    assert np.array_equal(out["perm"].cpu().numpy(), ref["perm"])
+    err = rel_err_per_token(y_to_f64(out["y"]), ref["y"])
+    assert err.max() <= 2e-2 and err.mean() <= 5e-3, (err.max(), err.mean())
+    q, s = moe.quant_fp8(x)
+    args = (out["perm"], out["offsets"], out["counts"], layer.slot_of_expert, layer.pool, layer.n_slots, layer.stride)
+    for dt in (torch.float32, torch.bfloat16):
+        a, _ = moe.expert_ffn_grouped(x, *args, "fp8", wl.f, wl.k, shared_w=layer.shared, y_dtype=dt)
+        b, ws = moe.expert_ffn_fp8(q, s, *args, wl.f, wl.k, shared_w=layer.shared, y_dtype=dt)
+        assert np.array_equal(_bits(a), _bits(b))
+        c, _ = moe.expert_ffn_fp8(q, s, *args, wl.f, wl.k, shared_w=layer.shared, y_dtype=dt, ws=ws)
+        assert np.array_equal(_bits(c), _bits(b))
+        assert int(ws[:4].view(torch.int32).item()) == 0
+    y16 = torch.empty_like(b)
+    moe.expert_ffn_grouped_noalloc(x, *args, "fp8", wl.f, wl.k, y16, shared_w=layer.shared)
+    assert np.array_equal(_bits(y16), _bits(b))
+
+
+@pytest.mark.parametrize("T", [2, 90, 400])
+def test_absent_and_elsewhere_slots(moe, T):
+    """An absent slot sets the status word and zeros its rows, MOE_SLOT_ELSEWHERE leaves them, the other
+    experts' rows keep their bits."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    wl = small_workload("bf16", "fp8", 256, 384, 6, 3, shared=True)
+    li = synth.layer_inputs(wl, T, seed=2)
+    layer = DeviceLayer.from_inputs(li)
+    x = layer.x_to_device(li.x)
+    forced = np.stack([np.random.default_rng(t).permutation(6)[:3] for t in range(T)]).astype(np.int32)
+    out = layer.forward(x, forced_idx=to_dev(forced, "i32"))
+    soe = layer.slot_of_expert.clone()
+    soe[1], soe[2], soe[4] = -1, layer.n_slots, -2
+    q, s = moe.quant_fp8(x)
+    y = torch.full_like(out["y_perm"], 123.0)
+    args = (out["perm"], out["offsets"], out["counts"])
+    _, ws = moe.expert_ffn_fp8(q, s, *args, soe, layer.pool, layer.n_slots, layer.stride, wl.f, wl.k,
+                               shared_w=layer.shared, y_perm=y)
+    off = out["offsets"].cpu().numpy()
+    for e in range(7):
+        rows = slice(off[e], off[e + 1]) if e < 6 else slice(T * 3, T * 4)
+        got = y[rows]
+        if e in (1, 2):
+            assert not got.any()
+        elif e == 4:
+            assert (got == 123.0).all()
+        else:
+            assert torch.equal(got, out["y_perm"][rows])
+    assert int(ws[:4].view(torch.int32).item()) == (1 if (np.isin(forced, [1, 2])).any() else 0)
+
+
+@pytest.mark.parametrize("wdt,act,T", [("fp8", "bf16", 1), ("fp8", "bf16", 130), ("bf16", "bf16", 9), ("f32", "f32", 5)])
+def test_layer_that_begins_with_its_norm(moe, wdt, act, T):
+    """Residual, norm, router, experts and combine as one layer call, against the oracle run on the norm
+    that the GPU kept; the same calls one by one give the same bits; buffers of a serving loop too."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    wl = small_workload(act, wdt, 256, 256, 8, 2, shared=True)
+    li = synth.layer_inputs(wl, T, seed=4)
+    rng = np.random.default_rng(9)
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    w = (1 + 0.2 * rng.normal(size=256)).astype(np.float32)
+    w_host = (w.view(np.uint32) >> 16).astype(np.uint16) if act == "bf16" else w
+    layer = DeviceLayer.from_inputs(li, norm_weight=w_host)
+    x = layer.x_to_device(li.x)
+    r = _rows(rng, T, 256, dt)
+    out = layer.forward(x, residual=r)
+    y, h, q, s = moe.add_rmsnorm(x, layer.norm_weight, residual=r, emit="both")
+    _check_norm(x, r, layer.norm_weight, 1e-6, y, h, q, s)
+    assert torch.equal(out["x"], y) and torch.equal(out["residual"], h)
+    plain = DeviceLayer.from_inputs(li)
+    if wdt == "fp8":
+        yp, _ = moe.expert_ffn_fp8(q, s, out["perm"], out["offsets"], out["counts"], plain.slot_of_expert, plain.pool,
+                                   plain.n_slots, plain.stride, wl.f, wl.k, shared_w=plain.shared,
+                                   y_dtype=out["y_perm"].dtype)
+        assert torch.equal(yp, out["y_perm"])
+    else:
+        assert torch.equal(plain.forward(y)["y"], out["y"])
+    tol, mean = (2e-2, 5e-3) if act == "bf16" else (1e-4, 1e-5)
+    host = _bits(out["x"]).view(np.uint16) if act == "bf16" else out["x"].cpu().numpy()
+    ref = moe_layer(host, li.w_router, li.bias, act, wl.k, wl.E, li.experts, li.shared)
+    y_ref = ref["y"]
+    if wdt == "fp8":
+        # the experts' rows are the norm's 8 bits, taken before its rounding to bf16: the oracle's experts run on
+        # the values they stand for (quantising those gives them back: a group's largest is 448 s, so its scale
+        # is s again, and q s (1/s) is q to within 2 u, far from a border between two e4m3 values)
+        xv = fp8.rows_value(fp8.decode(_bits(q)), s.cpu().numpy().astype(np.float64))
+        y_ref = fp8.swiglu_expert_fp8(xv, *expert_to_f64(li.shared))
+        for e in range(wl.E):
+            t, j = np.nonzero(ref["topk_idx"] == e)
+            y_ref[t] += ref["gates"][t, j][:, None] * fp8.swiglu_expert_fp8(xv[t], *expert_to_f64(li.experts[e]))
+    err = rel_err_per_token(y_to_f64(out["y"]), y_ref)
+    assert err.max() <= tol and err.mean() <= mean
+    bufs = layer.buffers(T)
+    for _ in range(2):
+        again = layer.forward(x, residual=r, bufs=bufs)
+        assert torch.equal(again["y"], out["y"]) and torch.equal(again["residual"], h)
+    assert layer.forward(x, bufs=bufs)["residual"] is None
+    with pytest.raises(ValueError, match="norm weight"):
+        plain.forward(x, residual=r)
+
+
+@pytest.mark.parametrize("T", [1, 24, 200])
+def test_block_in_a_graph(moe, T):
+    """A whole block (residual and norm, projections by the 8-bit product, the next layer's norm, fp8
+    experts) captured once and replayed: each replay gives the eager call's bits on its input, with
+    eager work on the same leaves between the replays."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    d = 512
+    wl = small_workload("bf16", "fp8", d, 256, 8, 2, shared=True)
+    li = synth.layer_inputs(wl, T, seed=6)
+    rng = np.random.default_rng(3)
+    ones = np.full(d, 0x3F80, np.uint16)
+    layer = DeviceLayer.from_inputs(li, norm_weight=ones)
+    g1 = (1 + 0.2 * _rows(rng, 1, d, torch.float32)[0]).to(torch.bfloat16)
+    _, (_, _, w, sw) = _operands(rng, 1, d, d)
+
+    def block(x, r, bufs):
+        _, h, q, s = moe.add_rmsnorm(x, g1, residual=r, emit="fp8")
+        return layer.forward(moe.gemm_fp8(q, s, w, sw), residual=h, bufs=bufs)
+
+    xs = [(_rows(rng, T, d, torch.bfloat16), _rows(rng, T, d, torch.bfloat16)) for _ in range(2)]
+    eager, inside = layer.buffers(T), layer.buffers(T)
+    refs = []
+    for x, r in xs:
+        o = block(x, r, eager)
+        refs.append((o["y"].clone(), o["residual"].clone()))
+    x_in, r_in = xs[0][0].clone(), xs[0][1].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block(x_in, r_in, inside)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = block(x_in, r_in, inside)
+    for b in (0, 1, 1, 0):
+        x_in.copy_(xs[b][0])
+        r_in.copy_(xs[b][1])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o["y"], refs[b][0]) and torch.equal(o["residual"], refs[b][1])
+        e = block(*xs[1 - b], eager)
+        torch.cuda.synchronize()
+        assert torch.equal(e["y"], refs[1 - b][0])
+    del g, o
+    gc.collect()
+
+
+def test_calls_on_two_streams_with_their_own_workspaces(moe):
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    wl = small_workload("bf16", "fp8", 512, 256, 8, 2)
+    li = synth.layer_inputs(wl, 96, seed=8)
+    layer = DeviceLayer.from_inputs(li)
+    x = layer.x_to_device(li.x)
+    out = layer.forward(x)
+    ref = out["y_perm"].clone()
+    args = (x, out["perm"], out["offsets"], out["counts"], layer.slot_of_expert, layer.pool, layer.n_slots,
+            layer.stride, "fp8", wl.f, wl.k)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [layer.workspace(96) for _ in streams]
+    ys = [[torch.empty_like(ref) for _ in range(4)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for st, w, y in zip(streams, ws, ys):
+            moe.expert_ffn_grouped(*args, y_perm=y[i], ws=w, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref) for per in ys for y in per)
+
+
+@pytest.mark.parametrize("mode", ["native", "split"])
+def test_offloaded_stack_of_fp8_experts(moe, mode):
+    """fp8 experts behind the slot cache: prefill and decode outputs are those of resident layers, and
+    the native decode steps (plain and split launches) give the call-by-call loop's bits."""
+    import torch
+    from expert_offload_cache_amd.offload import OffloadStack
+
+    L, E, K, T = 3, 8, 2, 90
+    wl = small_workload("bf16", "fp8", 256, 256, E, K, shared=True)
+    trace = synth.routing_trace(seed=3, steps=8, L=L, E=E, k=K)
+    stacks = [OffloadStack(wl, L, 18, seed=0, n_images=16, prefill_tokens=T) for _ in range(2)]
+    outs = []
+    try:
+        for st, kw in zip(stacks, (dict(native=False), dict(split_launch=mode == "split"))):
+            _, pre = st.prefill(keep_outputs=True)
+            _, dec = st.decode(trace, keep_outputs=True, **kw)
+            outs.append(([_bits(y) for _, y in pre], [(s, l, _bits(y)) for s, l, y in dec], pre))
+        for a, b in zip(outs[0][0], outs[1][0]):
+            assert np.array_equal(a, b)
+        for (s, l, a), (s2, l2, b) in zip(outs[0][1], outs[1][1]):
+            assert (s, l) == (s2, l2) and np.array_equal(a, b)
+        st = stacks[0]
+        for l, (idx, y) in enumerate(outs[0][2]):
+            experts = [synth.expert_weights(wl, 0, st.image_of(l, e) // E, st.image_of(l, e) % E) for e in range(E)]
+            shared = synth.expert_weights(wl, 0, st.shared_layer_of(l), 0, shared=True)
+            li = synth.layer_inputs(wl, T, 0, layer=l, batch=0, with_experts=False)
+            ref = moe_layer(li.x, li.w_router, li.bias, "bf16", K, E, experts, shared)
+            assert np.array_equal(idx.cpu().numpy(), ref["topk_idx"])
+            err = rel_err_per_token(y_to_f64(y), ref["y"])
+            assert err.max() <= 2e-2 and err.mean() <= 5e-3
+    finally:
+        for st in stacks:
+            st.close()
+        torch.cuda.synchronize()
