@@ -8,15 +8,35 @@ using namespace moe;
 
 namespace moe {
 
+// n rows of w e4m3 values and their scales behind them
+static size_t rows8_bytes(size_t n, int w) { return align_up(n * w, 256) + align_up(n * (w / 128) * 4, 256); }
+
 size_t ffn_fp8_workspace(int T, int d, int f, int k, int has_shared) {
-    (void)d;
     const size_t rows = (size_t)T * k + (has_shared ? (size_t)T : 0);
-    return kWsHeader + kPlanBytes + align_up(rows * f * 4, 256);
+    if (T <= kFp8Decode) return kWsHeader + kPlanBytes + align_up(rows * f * 4, 256);
+    return kWsHeader + kPlanBytes + rows8_bytes(T, d) + rows8_bytes(rows, f);
 }
 
-moe_status ffn_fp8_run(const FfnFp8& p, hipStream_t st) {
-    moe_status r = ffn_fp8_stream(p, kGateUp, st);
-    return r != MOE_OK ? r : ffn_fp8_stream(p, kDown, st);
+moe_status ffn_fp8_run(const FfnFp8& call, hipStream_t st) {
+    FfnFp8 p = call;
+    if (p.a.T <= kFp8Decode) {
+        moe_status r = ffn_fp8_stream(p, kGateUp, st);
+        return r != MOE_OK ? r : ffn_fp8_stream(p, kDown, st);
+    }
+    const size_t rows = (size_t)p.a.T * p.a.k + (p.a.shared_w ? (size_t)p.a.T : 0);
+    uint8_t* ws = (uint8_t*)p.a.h;
+    p.h8 = ws + rows8_bytes(p.a.T, p.a.d);
+    p.h_scale = (float*)(p.h8 + align_up(rows * p.a.f, 256));
+    p.x8 = (const uint8_t*)p.a.x;
+    if (!p.x_scale) {
+        float* scale = (float*)(ws + align_up((size_t)p.a.T * p.a.d, 256));
+        moe_status r = quant_rows_bf16(p.a.x, p.a.T, p.a.d, ws, scale, st);
+        if (r != MOE_OK) return r;
+        p.x8 = ws;
+        p.x_scale = scale;
+    }
+    moe_status r = ffn_fp8_tile(p, kGateUp, st);
+    return r != MOE_OK ? r : ffn_fp8_tile(p, kDown, st);
 }
 
 }  // namespace moe
@@ -53,6 +73,10 @@ moe_status moe_gemm_fp8(const void* a, size_t lda, const float* a_scale, int M, 
     g.G = fp8_groups(K);
     g.c_bf16 = out == MOE_BF16;
     g.c_vec = (uintptr_t)c % (4 * esz) == 0 && ldc % 4 == 0;
+    if (M > 256) {
+        moe_status r = gemm_fp8_tile(g, (hipStream_t)s);
+        if (r != MOE_EDTYPE) return r;
+    }
     return gemm_fp8_stream(g, (hipStream_t)s);
 }
 
@@ -61,7 +85,7 @@ moe_status moe_expert_ffn_fp8(const void* x, const float* x_scale, int T, int d,
                               const int32_t* slot_of_expert, int n_slots, const void* slot_pool, size_t slot_stride,
                               const void* shared_w, void* y_perm, moe_dtype y_dtype, void* ws, size_t ws_bytes,
                               moe_stream s) {
-    FfnFp8 p;
+    FfnFp8 p{};
     moe_status r = ffn_prepare(p.a, "moe_expert_ffn_fp8", x, MOE_FP8_B128, T, d, f, E, k, perm, offsets, counts,
                                slot_of_expert, n_slots, slot_pool, slot_stride, MOE_FP8_B128, shared_w, y_perm, y_dtype,
                                true);

@@ -22,15 +22,49 @@ struct GemmFp8 {
     int c_vec;   // four consecutive elements of c may be stored at once
 };
 
-// A grouped call: FfnArgs with x either bf16 rows (x_scale NULL, quantised as they are loaded) or
-// e4m3 rows with their scales; h holds the intermediate rows in binary32.
+// four consecutive columns n .. of row m of c
+__device__ __forceinline__ void store_c4(const GemmFp8& g, int m, int n, f32x4_t v) {
+    if (g.c_vec && n + 3 < g.N) {
+        if (g.c_bf16) {
+            uint2 o;
+            o.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
+            o.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
+            *(uint2*)((uint16_t*)g.c + (size_t)m * g.ldc + n) = o;
+        } else {
+            *(float4*)((float*)g.c + (size_t)m * g.ldc + n) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < g.N) {
+            if (g.c_bf16) ((uint16_t*)g.c)[(size_t)m * g.ldc + n + i] = f32_to_bf16(v[i]);
+            else ((float*)g.c)[(size_t)m * g.ldc + n + i] = v[i];
+        }
+}
+
+// A grouped call: FfnArgs with x either bf16 rows (x_scale NULL) or e4m3 rows with their scales.
+// Up to kFp8Decode tokens, a.h holds the intermediate rows in binary32 and bf16 rows are quantised as
+// they are loaded; above, x8 / x_scale hold the rows in 8 bits, h8 / h_scale the intermediate rows.
 struct FfnFp8 {
     FfnArgs a;
     const float* x_scale;
+    const uint8_t* x8 = nullptr;
+    uint8_t* h8 = nullptr;
+    float* h_scale = nullptr;
 };
+constexpr int kFp8Decode = 64;
 
+// bf16 rows [T, d], back to back, into e4m3 rows and scales (norm.hip)
+moe_status quant_rows_bf16(const void* x, int T, int d, uint8_t* q, float* scale, hipStream_t st);
+
+// few rows (fp8_stream.hip): the weights are streamed once
 moe_status gemm_fp8_stream(const GemmFp8& g, hipStream_t st);
 moe_status ffn_fp8_stream(const FfnFp8& f, int mode, hipStream_t st);
+// many rows (fp8_tile.hip); gemm_fp8_tile returns MOE_EDTYPE, with nothing launched, where it does
+// not apply
+moe_status gemm_fp8_tile(const GemmFp8& g, hipStream_t st);
+moe_status ffn_fp8_tile(const FfnFp8& f, int mode, hipStream_t st);
 // both projections of a grouped call with 8-bit weights
 moe_status ffn_fp8_run(const FfnFp8& f, hipStream_t st);
 size_t ffn_fp8_workspace(int T, int d, int f, int k, int has_shared);

@@ -184,26 +184,6 @@ __device__ __forceinline__ void join_waves(const f32x4_t (&acc)[NU], int w, int 
 }
 
 // ---- the dense product ----------------------------------------------------------------------------
-__device__ __forceinline__ void store_c4(const GemmFp8& g, int m, int n, f32x4_t v) {
-    if (g.c_vec && n + 3 < g.N) {
-        if (g.c_bf16) {
-            uint2 o;
-            o.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
-            o.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
-            *(uint2*)((uint16_t*)g.c + (size_t)m * g.ldc + n) = o;
-        } else {
-            *(float4*)((float*)g.c + (size_t)m * g.ldc + n) = make_float4(v[0], v[1], v[2], v[3]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (n + i < g.N) {
-            if (g.c_bf16) ((uint16_t*)g.c)[(size_t)m * g.ldc + n + i] = f32_to_bf16(v[i]);
-            else ((float*)g.c)[(size_t)m * g.ldc + n + i] = v[i];
-        }
-}
-
 template <int RB, int TB, int D, bool TAIL>
 __global__ __launch_bounds__(512) void gemm_fp8_stream_kernel(GemmFp8 g) {
     extern __shared__ __align__(16) uint8_t smem[];

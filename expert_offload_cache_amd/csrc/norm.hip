@@ -12,7 +12,7 @@
 // the width alone, so a row's bits do not depend on how many rows the call has.
 #include <hip/hip_runtime.h>
 
-#include "fp8.h"
+#include "fp8_ops.h"
 
 namespace moe {
 namespace {
@@ -203,6 +203,18 @@ constexpr int kMaxRow = 16384;
 size_t elem(moe_dtype t) { return t == MOE_BF16 ? 2 : 4; }
 
 }  // namespace
+
+moe_status quant_rows_bf16(const void* x, int T, int d, uint8_t* q, float* scale, hipStream_t st) {
+    RowArgs a{};
+    a.x = x;
+    a.q = q;
+    a.scale = scale;
+    a.T = T;
+    a.d = d;
+    a.ldx = a.ldq = (size_t)d;
+    return run_rows<uint16_t, uint16_t, false>(a, st, "quant_fp8_bf16");
+}
+
 }  // namespace moe
 
 using namespace moe;
