@@ -58,9 +58,11 @@ def _p(t) -> Optional[int]:
 
 
 def _s(stream) -> Optional[int]:
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current device's current stream, as a handle: torch.cuda.current_stream() builds a Stream
+        # object around it, 2.9 us of a call whose kernel may take 4
+        C = _torch()._C
+        return C._cuda_getCurrentRawStream(C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -174,37 +176,43 @@ def expert_ffn_grouped_noalloc(x, perm, offsets, counts, slot_of_expert, slot_po
     return y_perm
 
 
-def _on_current_device(*ts):
+def _on_current_device(*ts) -> None:
     """The library launches on the current device: every tensor has to live there."""
-    torch = _torch()
-    dev = torch.cuda.current_device()
+    dev = -1
     for t in ts:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+        if t is not None:
+            if dev < 0 <= t.get_device():
+                dev = _torch()._C._cuda_getDevice()
+            if dev < 0 or t.get_device() != dev:
+                raise ValueError(f"tensors must be on the current GPU, got {t.device}")
 
 
-def _rows(name, t, T: int, d: int, dtype) -> int:
+def _rows(name, t, shape, dtype) -> int:
     """Checks a [T, d] tensor of dense rows; -> elements from a row to the next."""
-    if t.dtype != dtype or tuple(t.shape) != (T, d):
-        raise ValueError(f"{name} must be {dtype} [{T}, {d}], got {t.dtype} {list(t.shape)}")
-    if d > 1 and t.stride(1) != 1:
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must lie next to each other")
-    return t.stride(0) if T > 1 else d
+    return ld if shape[0] > 1 else shape[1]
 
 
-def _dense(name, t, shape, dtype):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _dense(name, t, shape, dtype) -> None:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-def _quantised_out(x, T: int, d: int, out):
+def _quantised_out(x, shape, q, scale):
+    """The given (or new) e4m3 rows and scales of `shape` -> (q, scale, elements from a row of q to the next)."""
     torch = _torch()
-    if out[0] is None:
-        out = (torch.empty((T, d), dtype=torch.float8_e4m3fn, device=x.device),
-               torch.empty((T, (d + 127) // 128), dtype=torch.float32, device=x.device))
-    q, scale = out
-    ldq = _rows("q", q, T, d, torch.float8_e4m3fn)
-    _dense("scale", scale, (T, (d + 127) // 128), torch.float32)
+    groups = (shape[0], (shape[1] + 127) // 128)
+    if q is None and scale is None:
+        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty(groups, dtype=torch.float32, device=x.device)
+    elif q is None or scale is None:
+        raise ValueError("q and scale come together")
+    ldq = _rows("q", q, shape, torch.float8_e4m3fn)
+    _dense("scale", scale, groups, torch.float32)
     return q, scale, ldq
 
 
@@ -214,41 +222,46 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, emit: str = "y", ou
     out: the returned tuple's tensors to write into (None where not emitted).
     -> (y, h, q, scale), None where there is none (h: without a residual)."""
     torch = _torch()
+    act = _act(x)
+    shape, dt = x.shape, x.dtype
+    T, d = shape
     if emit not in ("y", "fp8", "both"):
         raise ValueError(f'emit must be "y", "fp8" or "both", got {emit!r}')
-    act = _act(x)
-    T, d = x.shape
-    y, h, q, scale = out if out is not None else (None, None, None, None)
-    if out is None and emit != "fp8":
-        y = torch.empty((T, d), dtype=x.dtype, device=x.device)
-    if out is None and residual is not None:
-        h = torch.empty((T, d), dtype=x.dtype, device=x.device)
-    ldq = 0
-    if emit != "y":
-        q, scale, ldq = _quantised_out(x, T, d, (q, scale))
-    elif q is not None or scale is not None:
-        raise ValueError('out holds q or scale, but emit is "y"')
-    if (y is None) != (emit == "fp8"):
-        raise ValueError(f"emit {emit!r} and out's y do not agree")
+    if out is None:
+        y = torch.empty(shape, dtype=dt, device=x.device) if emit != "fp8" else None
+        h = torch.empty(shape, dtype=dt, device=x.device) if residual is not None else None
+        q = scale = None
+    else:
+        y, h, q, scale = out
+        if (y is None) != (emit == "fp8"):
+            raise ValueError(f"emit {emit!r} and out's y do not agree")
+        if emit == "y" and (q is not None or scale is not None):
+            raise ValueError('out holds q or scale, but emit is "y"')
     if (residual is None) != (h is None):
         raise ValueError("a residual and its sum in out come together")
+    ldr = ldh = ldy = ldq = 0
+    if residual is not None:
+        ldr, ldh = _rows("residual", residual, shape, dt), _rows("h", h, shape, dt)
+    if y is not None:
+        ldy = _rows("y", y, shape, dt)
+    if emit != "y":
+        q, scale, ldq = _quantised_out(x, shape, q, scale)
+    w_code = act if weight.dtype == dt else MOE_F32
+    _dense("weight", weight, (d,), dt if w_code == act else torch.float32)
     _on_current_device(x, weight, residual, y, h, q, scale)
-    w_code = act if weight.dtype == x.dtype else MOE_F32
-    _dense("weight", weight, (d,), x.dtype if w_code == act else torch.float32)
-    check(lib().moe_add_rmsnorm(_p(x), act, T, d, _rows("x", x, T, d, x.dtype), _p(residual),
-                                0 if residual is None else _rows("residual", residual, T, d, x.dtype), _p(weight), w_code,
-                                eps, _p(h), 0 if h is None else _rows("h", h, T, d, x.dtype), _p(y),
-                                0 if y is None else _rows("y", y, T, d, x.dtype), _p(q), ldq, _p(scale), _s(stream)))
+    check(lib().moe_add_rmsnorm(_p(x), act, T, d, _rows("x", x, shape, dt), _p(residual), ldr, _p(weight), w_code, eps,
+                                _p(h), ldh, _p(y), ldy, _p(q), ldq, _p(scale), _s(stream)))
     return y, h, q, scale
 
 
 def quant_fp8(x, out=None, stream=None):
     """Rows [T, d] -> (q e4m3 [T, d], scale f32 [T, ceil(d / 128)]) (moe_quant_fp8)."""
     act = _act(x)
-    T, d = x.shape
-    q, scale, ldq = _quantised_out(x, T, d, out if out is not None else (None, None))
+    shape = x.shape
+    T, d = shape
+    q, scale, ldq = _quantised_out(x, shape, *(out if out is not None else (None, None)))
     _on_current_device(x, q, scale)
-    check(lib().moe_quant_fp8(_p(x), act, T, d, _rows("x", x, T, d, x.dtype), _p(q), ldq, _p(scale), _s(stream)))
+    check(lib().moe_quant_fp8(_p(x), act, T, d, _rows("x", x, shape, x.dtype), _p(q), ldq, _p(scale), _s(stream)))
     return q, scale
 
 
@@ -265,13 +278,13 @@ def gemm_fp8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None):
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"the result must be bfloat16 or float32, got {out.dtype}")
-    lda, ldw = _rows("a", a, M, K, torch.float8_e4m3fn), _rows("w", w, N, K, torch.float8_e4m3fn)
+    e4m3 = torch.float8_e4m3fn
+    lda, ldw, ldc = _rows("a", a, (M, K), e4m3), _rows("w", w, (N, K), e4m3), _rows("out", out, (M, N), out.dtype)
     _dense("a_scale", a_scale, (M, G), torch.float32)
     _dense("w_scale", w_scale, ((N + 127) // 128, G), torch.float32)
     _on_current_device(a, a_scale, w, w_scale, out)
-    check(lib().moe_gemm_fp8(_p(a), lda, _p(a_scale), M, K, _p(w), ldw, _p(w_scale), N, _p(out),
-                             _rows("out", out, M, N, out.dtype), MOE_BF16 if out.dtype == torch.bfloat16 else MOE_F32,
-                             _s(stream)))
+    check(lib().moe_gemm_fp8(_p(a), lda, _p(a_scale), M, K, _p(w), ldw, _p(w_scale), N, _p(out), ldc,
+                             MOE_BF16 if out.dtype == torch.bfloat16 else MOE_F32, _s(stream)))
     return out
 
 
