@@ -13,28 +13,28 @@ static size_t rows8_bytes(size_t n, int w) { return align_up(n * w, 256) + align
 
 size_t ffn_fp8_workspace(int T, int d, int f, int k, int has_shared) {
     const size_t rows = (size_t)T * k + (has_shared ? (size_t)T : 0);
-    if (T <= kFp8Decode) return kWsHeader + kPlanBytes + align_up(rows * f * 4, 256);
-    return kWsHeader + kPlanBytes + rows8_bytes(T, d) + rows8_bytes(rows, f);
+    return kWsHeader + kPlanBytes +
+           (T <= kFp8Stream ? align_up(rows * f * 4, 256) : rows8_bytes(T, d) + rows8_bytes(rows, f));
 }
 
 moe_status ffn_fp8_run(const FfnFp8& call, hipStream_t st) {
     FfnFp8 p = call;
-    if (p.a.T <= kFp8Decode) {
+    p.x8 = p.x_scale ? (const uint8_t*)p.a.x : nullptr;
+    if (p.a.T <= kFp8Stream) {
         moe_status r = ffn_fp8_stream(p, kGateUp, st);
         return r != MOE_OK ? r : ffn_fp8_stream(p, kDown, st);
     }
-    const size_t rows = (size_t)p.a.T * p.a.k + (p.a.shared_w ? (size_t)p.a.T : 0);
     uint8_t* ws = (uint8_t*)p.a.h;
-    p.h8 = ws + rows8_bytes(p.a.T, p.a.d);
-    p.h_scale = (float*)(p.h8 + align_up(rows * p.a.f, 256));
-    p.x8 = (const uint8_t*)p.a.x;
-    if (!p.x_scale) {
+    if (!p.x8) {
         float* scale = (float*)(ws + align_up((size_t)p.a.T * p.a.d, 256));
         moe_status r = quant_rows_bf16(p.a.x, p.a.T, p.a.d, ws, scale, st);
         if (r != MOE_OK) return r;
         p.x8 = ws;
         p.x_scale = scale;
     }
+    const size_t rows = (size_t)p.a.T * p.a.k + (p.a.shared_w ? (size_t)p.a.T : 0);
+    p.h8 = ws + rows8_bytes(p.a.T, p.a.d);
+    p.h_scale = (float*)(p.h8 + align_up(rows * p.a.f, 256));
     moe_status r = ffn_fp8_tile(p, kGateUp, st);
     return r != MOE_OK ? r : ffn_fp8_tile(p, kDown, st);
 }

@@ -44,8 +44,9 @@ __device__ __forceinline__ void store_c4(const GemmFp8& g, int m, int n, f32x4_t
 }
 
 // A grouped call: FfnArgs with x either bf16 rows (x_scale NULL) or e4m3 rows with their scales.
-// Up to kFp8Decode tokens, a.h holds the intermediate rows in binary32 and bf16 rows are quantised as
-// they are loaded; above, x8 / x_scale hold the rows in 8 bits, h8 / h_scale the intermediate rows.
+// The streaming kernels (calls of up to kFp8Stream tokens) keep the intermediate rows of h in binary32 (a.h)
+// and quantise them, and bf16 rows of x where x8 is NULL, as they load them; the tiles read x8 / x_scale
+// and keep h8 / h_scale.
 struct FfnFp8 {
     FfnArgs a;
     const float* x_scale;
@@ -53,7 +54,7 @@ struct FfnFp8 {
     uint8_t* h8 = nullptr;
     float* h_scale = nullptr;
 };
-constexpr int kFp8Decode = 64;
+constexpr int kFp8Stream = 16;
 
 // bf16 rows [T, d], back to back, into e4m3 rows and scales (norm.hip)
 moe_status quant_rows_bf16(const void* x, int T, int d, uint8_t* q, float* scale, hipStream_t st);

@@ -183,6 +183,64 @@ __device__ __forceinline__ void join_waves(const f32x4_t (&acc)[NU], int w, int 
     }
 }
 
+// ---- up to 16 tokens ----------------------------------------------------------------------------------
+// One token block, RBW row blocks a workgroup: the wave's token operands (NS steps) are prepared once and stay
+// in registers, and its RBW * NS weight fragments stream through a ring of D.  frag(i, ks): this lane's
+// first 16 bytes of row block i at step ks, the second half `whalf` bytes on; wscale(i): the block's scales.
+// EVEN: S * NS = nst, every wave has NS steps; else wave w has those of w, w + S, ... that exist.
+template <int SRC, int NS, int RBW, int D, bool EVEN, bool TAIL, typename FP, typename SP>
+__device__ __forceinline__ void stream_rows(FP&& frag, SP&& wscale, int whalf, const uint8_t* xrow, const float* xscale,
+                                            int nst, int w, int S, int K, f32x4_t (&acc)[RBW]) {
+    constexpr int EB = SrcOf<SRC>::kBytes;
+    const int q = (threadIdx.x & 63) >> 4;
+    const int n = EVEN ? NS : min(NS, max(0, (nst - w + S - 1) / S));
+    u32x4_t rw[D][2];
+    float rs[D];
+    auto load = [&](int idx) __attribute__((always_inline)) {
+        const int i = idx / NS, t = idx % NS, ks = w + t * S;
+        if (!EVEN && t >= n) return;
+        const bool in0 = !TAIL || ks * 128 + 16 * q < K, in1 = !TAIL || ks * 128 + 64 + 16 * q < K;
+        const uint8_t* p = frag(i, ks);
+        rw[idx % D][0] = __builtin_nontemporal_load((const u32x4_t*)(in0 ? p : g_zero16));
+        rw[idx % D][1] = __builtin_nontemporal_load((const u32x4_t*)(in1 ? p + whalf : g_zero16));
+        rs[idx % D] = wscale(i)[ks];
+    };
+#pragma unroll
+    for (int idx = 0; idx < (D < RBW * NS ? D : RBW * NS); ++idx) load(idx);
+    constexpr bool kWide = NS <= 2;  // few steps: their tokens are kept as bf16
+    Wide8 xw[kWide ? NS : 1];
+    i32x8_t xr[kWide ? 1 : NS];
+    float xs[NS];
+#pragma unroll
+    for (int t = 0; t < NS; ++t) {
+        if (!EVEN && t >= n) continue;
+        const int ks = w + t * S;
+        const bool in0 = !TAIL || ks * 128 + 16 * q < K, in1 = !TAIL || ks * 128 + 64 + 16 * q < K;
+        const uint8_t* p = xrow + ((size_t)ks * 128 + 16 * q) * EB;
+        u32x4_t x[2 * EB];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < EB; ++c) x[h * EB + c] = *(const u32x4_t*)((h ? in1 : in0) ? p + h * 64 * EB + 16 * c : g_zero16);
+        if constexpr (SRC == kSrcFp8) xs[t] = xscale[ks];
+        if constexpr (kWide) xw[t] = widen(token_operand<SRC>(x, xs[t]));
+        else xr[t] = token_operand<SRC>(x, xs[t]);
+    }
+#pragma unroll
+    for (int i = 0; i < RBW; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int idx = 0; idx < RBW * NS; ++idx) {
+        const int i = idx / NS, t = idx % NS;
+        if (EVEN || t < n) {
+            const f32x4_t p = mfma_fp8_exact(widen(join8(rw[idx % D][0], rw[idx % D][1])), kWide ? xw[kWide ? t : 0] : widen(xr[kWide ? 0 : t]));
+            const float f = rs[idx % D] * xs[t];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_fmaf(p[c], f, acc[i][c]);
+        }
+        if (idx + D < RBW * NS) load(idx + D);
+    }
+}
+
 // ---- the dense product ----------------------------------------------------------------------------
 template <int RB, int TB, int D, bool TAIL>
 __global__ __launch_bounds__(512) void gemm_fp8_stream_kernel(GemmFp8 g) {
@@ -226,15 +284,15 @@ moe_status launch_gemm(const GemmFp8& g, int S, hipStream_t st) {
 }
 
 // ---- the routed experts' projections ----------------------------------------------------------------
-template <int MODE, int SRC, int RB, int D>
-__global__ __launch_bounds__(512) void ffn_fp8_stream_kernel(FfnFp8 p) {
-    static_assert(MODE == kDown || RB % 2 == 0, "gate/up rows come in gate/up pairs");
+template <int MODE, int SRC, int NS, int RBW, int D, bool EVEN>
+__global__ __launch_bounds__(NS == 8 ? 1024 : 512, 4) void ffn_fp8_stream_kernel(FfnFp8 p) {
+    static_assert(MODE == kDown || RBW % 2 == 0, "gate/up rows come in gate/up pairs");
     extern __shared__ __align__(16) uint8_t smem[];
     const FfnArgs& a = p.a;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), S = blockDim.x >> 6;
     const int K = MODE == kGateUp ? a.d : a.f;
-    const int b0 = blockIdx.x * RB;  // first row block
+    const int b0 = blockIdx.x * RBW;  // first row block
     int e, chunk, slot, n_all, p0;
     if (!find_item(a, 16, blockIdx.y, e, chunk, slot, n_all, p0)) return;
     const bool shared = e == -1;
@@ -247,71 +305,101 @@ __global__ __launch_bounds__(512) void ffn_fp8_stream_kernel(FfnFp8 p) {
         if (slot < 0 || slot >= a.n_slots) {     // absent: flagged, zero rows (h is not read then)
             if (threadIdx.x == 0) *a.status = 1;
             if (MODE == kDown)
-                for (int i = threadIdx.x; i < nt * RB * 16; i += blockDim.x) {
-                    const int c = b0 * 16 + i % (RB * 16);
-                    if (c < a.d) store_y(a, (size_t)(p0 + t0 + i / (RB * 16)), c, 0.f);
+                for (int i = threadIdx.x; i < nt * RBW * 16; i += blockDim.x) {
+                    const int c = b0 * 16 + i % (RBW * 16);
+                    if (c < a.d) store_y(a, (size_t)(p0 + t0 + i / (RBW * 16)), c, 0.f);
                 }
             return;
         }
         base = a.pool + (size_t)slot * a.stride;
     }
-    Operands<RB, 1> o;
-    o.wstep = kFp8Frag;
-    o.whalf = kFp8Frag / 2;
     const int nblk = MODE == kGateUp ? 2 * (a.f / 16) : a.d / 16;
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        const int b = min(b0 + i, nblk - 1);
-        const uint8_t* blk = base + (MODE == kGateUp ? gu_block_offset(b >> 1, b & 1, a.d, MOE_FP8_B128)
-                                                     : down_block_offset(b, a.d, a.f, MOE_FP8_B128));
-        o.wp[i] = blk + lane * 16;
-        o.wsc[i] = (const float*)(blk + (size_t)16 * K);
-    }
+    const size_t rbb = rowblock_bytes(K, MOE_FP8_B128);
+    if (MODE == kDown) base += down_block_offset(0, a.d, a.f, MOE_FP8_B128);
+    // blocks past the end repeat the last one and are not stored
+    auto block = [&](int i) __attribute__((always_inline)) { return base + (size_t)min(b0 + i, nblk - 1) * rbb; };
+    auto frag = [&](int i, int ks) __attribute__((always_inline)) { return block(i) + (size_t)ks * kFp8Frag + lane * 16; };
+    auto wscale = [&](int i) __attribute__((always_inline)) { return (const float*)(block(i) + (size_t)16 * K); };
     const int row = p0 + t0 + min(lane & 15, nt - 1);  // lanes past the last token repeat it
     int src = row;
     if (MODE == kGateUp) src = shared ? row - a.T * a.k : a.perm[row] / a.k;
-    o.xp[0] = (const uint8_t*)(MODE == kGateUp ? a.x : a.h) + (size_t)src * K * SrcOf<SRC>::kBytes;
-    o.xsc[0] = SRC == kSrcFp8 ? p.x_scale + (size_t)src * (K / 128) : nullptr;
-    f32x4_t acc[RB][1];
-    stream<SRC, RB, 1, D, false>(o, K / 128, w, S, K, acc);
+    const uint8_t* x = MODE == kDown ? (const uint8_t*)a.h : SRC == kSrcFp8 ? p.x8 : (const uint8_t*)a.x;
+    f32x4_t acc[RBW];
+    stream_rows<SRC, NS, RBW, D, EVEN, false>(frag, wscale, kFp8Frag / 2, x + (size_t)src * K * SrcOf<SRC>::kBytes,
+                                              SRC == kSrcFp8 ? p.x_scale + (size_t)src * (K / 128) : nullptr, K / 128, w, S,
+                                              K, acc);
     const bool mine = (lane & 15) < nt;
     const size_t orow = (size_t)(p0 + t0 + (lane & 15));
-    if constexpr (MODE == kGateUp) {
-        // a unit is a gate block and its up block: SwiGLU where their sums meet
-        float4* red = (float4*)smem;
+    float4* red = (float4*)smem;
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-            red[((size_t)w * RB + i) * 64 + lane] = make_float4(acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]);
-        __syncthreads();
-        for (int u = w; u < RB / 2; u += S) {
-            float4 g = make_float4(0.f, 0.f, 0.f, 0.f), v = g;
-            for (int q = 0; q < S; ++q) {
-                const float4 tg = red[((size_t)q * RB + 2 * u) * 64 + lane], tu = red[((size_t)q * RB + 2 * u + 1) * 64 + lane];
-                g.x += tg.x, g.y += tg.y, g.z += tg.z, g.w += tg.w;
-                v.x += tu.x, v.y += tu.y, v.z += tu.z, v.w += tu.w;
-            }
+    for (int i = 0; i < RBW; ++i) red[((size_t)w * RBW + i) * 64 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    __syncthreads();
+    auto joined = [&](int i) __attribute__((always_inline)) {  // the waves' sums of row block i, in wave order
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int o = 0; o < S; ++o) {
+            const float4 t = red[((size_t)o * RBW + i) * 64 + lane];
+            v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+        }
+        return v;
+    };
+    if constexpr (MODE == kGateUp) {
+        for (int u = w; u < RBW / 2; u += S) {  // a gate block and its up block: SwiGLU where their sums meet
+            const float4 g = joined(2 * u), v = joined(2 * u + 1);
             const int c = (b0 / 2 + u) * 16 + 4 * (lane >> 4);
             if (mine && c < a.f)
                 *(float4*)((float*)a.h + orow * a.f + c) =
                     make_float4(silu_mul(g.x, v.x), silu_mul(g.y, v.y), silu_mul(g.z, v.z), silu_mul(g.w, v.w));
         }
     } else {
-        join_waves(*(const f32x4_t(*)[RB])&acc, w, S, (float4*)smem, [&](int u, f32x4_t v) {
+        for (int u = w; u < RBW; u += S) {
+            const float4 v = joined(u);
             const int c = (b0 + u) * 16 + 4 * (lane >> 4);
-            if (mine && c < a.d) store_y4(a, orow, c, v[0], v[1], v[2], v[3]);
-        });
+            if (mine && c < a.d) store_y4(a, orow, c, v.x, v.y, v.z, v.w);
+        }
     }
 }
 
-template <int MODE, int SRC, int RB, int D>
-moe_status launch_ffn(const FfnFp8& p, int S, hipStream_t st, const char* name) {
+template <int MODE, int SRC, int NS, int RBW, int D, bool EVEN>
+moe_status launch_rows(const FfnFp8& p, int S, hipStream_t st, const char* name) {
     const int nblk = MODE == kGateUp ? 2 * (p.a.f / 16) : p.a.d / 16;
     const int64_t items = work_items(p.a, 16);
     if (items > 65535) return set_error(MOE_ESHAPE, "%s: %lld work items exceed one launch", name, (long long)items);
-    const int lds = S * RB * 1024;
+    if (items <= 0) return MOE_OK;
+    const int lds = S * RBW * 1024;
+    auto kern = ffn_fp8_stream_kernel<MODE, SRC, NS, RBW, D, EVEN>;
+    if (lds > 65536) MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     ProfScope sc(name, st);
-    ffn_fp8_stream_kernel<MODE, SRC, RB, D><<<dim3((unsigned)((nblk + RB - 1) / RB), (unsigned)items), 64 * S, lds, st>>>(p);
+    kern<<<dim3((unsigned)((nblk + RBW - 1) / RBW), (unsigned)items), 64 * S, lds, st>>>(p);
     return check_launch(name);
+}
+
+// S waves that split nst steps, NS each at most
+struct Split {
+    int S, NS;
+    bool even;
+};
+Split split_steps(int nst) {
+    for (int ns = 1; ns <= 4; ns *= 2)  // 4 to 8 waves without a rest
+        if (nst % ns == 0 && nst / ns >= 4 && nst / ns <= 8) return {nst / ns, ns, true};
+    if (nst < 4) return {nst, 1, true};
+    int ns = 1;
+    while ((nst + ns - 1) / ns > (ns < 8 ? 8 : 16)) ns *= 2;
+    return {(nst + ns - 1) / ns, ns, false};
+}
+
+template <int MODE, int SRC>
+moe_status launch_split(const FfnFp8& p, hipStream_t st, const char* name) {
+    const Split sp = split_steps((MODE == kGateUp ? p.a.d : p.a.f) / 128);
+    constexpr int RBW = 4;
+    if (sp.even) {
+        if (sp.NS == 1) return launch_rows<MODE, SRC, 1, RBW, 4, true>(p, sp.S, st, name);
+        if (sp.NS == 2) return launch_rows<MODE, SRC, 2, RBW, 8, true>(p, sp.S, st, name);
+        return launch_rows<MODE, SRC, 4, RBW, 8, true>(p, sp.S, st, name);
+    }
+    if (sp.NS == 1) return launch_rows<MODE, SRC, 1, RBW, 4, false>(p, sp.S, st, name);
+    if (sp.NS == 2) return launch_rows<MODE, SRC, 2, RBW, 4, false>(p, sp.S, st, name);
+    if (sp.NS == 4) return launch_rows<MODE, SRC, 4, RBW, 4, false>(p, sp.S, st, name);
+    return launch_rows<MODE, SRC, 8, RBW, 4, false>(p, sp.S, st, name);
 }
 
 }  // namespace
@@ -324,10 +412,9 @@ moe_status gemm_fp8_stream(const GemmFp8& g, hipStream_t st) {
 }
 
 moe_status ffn_fp8_stream(const FfnFp8& p, int mode, hipStream_t st) {
-    const int S = std::min(8, (mode == kGateUp ? p.a.d : p.a.f) / 128);
-    if (mode == kDown) return launch_ffn<kDown, kSrcF32, 2, 2>(p, S, st, "ffn_fp8_down");
-    if (p.x_scale) return launch_ffn<kGateUp, kSrcFp8, 2, 4>(p, S, st, "ffn_fp8_gateup");
-    return launch_ffn<kGateUp, kSrcBf16, 2, 4>(p, S, st, "ffn_fp8_gateup");
+    if (mode == kDown) return launch_split<kDown, kSrcF32>(p, st, "ffn_fp8_down");
+    if (p.x8) return launch_split<kGateUp, kSrcFp8>(p, st, "ffn_fp8_gateup");
+    return launch_split<kGateUp, kSrcBf16>(p, st, "ffn_fp8_gateup");
 }
 
 }  // namespace moe
