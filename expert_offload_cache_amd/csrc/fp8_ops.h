@@ -61,10 +61,11 @@ moe_status quant_rows_bf16(const void* x, int T, int d, uint8_t* q, float* scale
 
 // few rows (fp8_stream.hip): the weights are streamed once
 moe_status gemm_fp8_stream(const GemmFp8& g, hipStream_t st);
+float gemm_fp8_stream_us(const GemmFp8& g);
 moe_status ffn_fp8_stream(const FfnFp8& f, int mode, hipStream_t st);
-// many rows (fp8_tile.hip); gemm_fp8_tile returns MOE_EDTYPE, with nothing launched, where it does
-// not apply
-moe_status gemm_fp8_tile(const GemmFp8& g, hipStream_t st);
+// many rows (fp8_tile.hip): the tile with the least estimated time (us; NULL: none applies), its launch
+const void* gemm_fp8_best_tile(const GemmFp8& g, float& us);
+moe_status gemm_fp8_tile(const GemmFp8& g, const void* tile, hipStream_t st);
 moe_status ffn_fp8_tile(const FfnFp8& f, int mode, hipStream_t st);
 // both projections of a grouped call with 8-bit weights
 moe_status ffn_fp8_run(const FfnFp8& f, hipStream_t st);

@@ -404,11 +404,22 @@ moe_status launch_split(const FfnFp8& p, hipStream_t st, const char* name) {
 
 }  // namespace
 
+// Estimated time (us) where a tile may be faster: 3.5 us and, for each 128-input step of a wave, 1.6 us (up to
+// 32 rows: 16 weight rows a workgroup) or 2.35 us (32 weight rows, 32 tokens) for each round of 512 or 256
+// workgroups.  Up to 16 rows: no tile is faster.
+float gemm_fp8_stream_us(const GemmFp8& g) {
+    const int steps = (g.G + 7) / 8;
+    if (g.M <= 16) return 0.f;
+    if (g.M <= 32) return 3.5f + steps * 1.6f * ((g.N + 16 * 512 - 1) / (16 * 512));
+    const int64_t wgs = (int64_t)((g.N + 31) / 32) * ((g.M + 31) / 32);
+    return 3.5f + steps * 2.35f * (float)((wgs + 255) / 256);
+}
+
 moe_status gemm_fp8_stream(const GemmFp8& g, hipStream_t st) {
     const int S = std::min(8, g.G);
     if (g.M <= 16) return launch_gemm<1, 1, 4>(g, S, st);
-    if (g.M <= 32) return launch_gemm<2, 2, 4>(g, S, st);
-    return launch_gemm<2, 4, 1>(g, S, st);
+    if (g.M <= 32) return launch_gemm<1, 2, 4>(g, S, st);
+    return launch_gemm<2, 2, 2>(g, S, st);
 }
 
 moe_status ffn_fp8_stream(const FfnFp8& p, int mode, hipStream_t st) {

@@ -6,7 +6,7 @@
 // block), whose sum is added to binary32 accumulators times the token's scale and the row block's.
 //
 // Both operands go through LDS by direct-to-LDS loads: the tokens, which every wave reads, in a ring of
-// three steps; each wave's weight rows in a ring of RW steps of its own.  (Weights straight into
+// RX steps; each wave's weight rows in a ring of RW steps of its own.  (Weights straight into
 // registers take two register sets, which does not leave room for the products in flight: experts of
 // 8192 tokens 1.69 ms against 1.61; and operand-order loads of a row-major matrix touch 16 rows at a
 // time.)  The scales of the whole tile are put into LDS once, before the first step.
@@ -66,20 +66,20 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("" ::: "memory");
 }
 
-template <int RA, int NTB, int NW, int RW>
+template <int RA, int NTB, int NW, int RW, int RX>
 struct Tile8 {
     static constexpr int kMT = NW * RA * 16, kNT = NTB * 16;
     static constexpr int kStage = NTB * kFp8Frag;
     static constexpr int kUnits = 2 * NTB / NW;  // 1 KB halves of a token block each wave loads a step
-    static constexpr int kRing = 3;
     static constexpr int kWBytes = kMT * kFp8Group;             // the waves' weight rows of one step
-    static constexpr int kScales = kRing * kStage + RW * kWBytes;  // where the scales begin
+    static constexpr int kScales = RX * kStage + RW * kWBytes;  // where the scales begin
     static constexpr int kWScales = kMT >= 128 ? kMT / 128 : 1;  // weight scales a step
     static_assert(kUnits * NW == 2 * NTB, "token blocks must divide over the waves");
     static_assert(NTB % 2 == 0 && NTB >= 4 && RA <= 4, "pipeline shape");
+    static_assert(RX >= 3 && RX >= RW && RX <= RW + 3, "the waits count on loads of both operands between two of one");
     // scales of step g: the tokens' at g * (kNT + 1), then (after G steps) the weights'
     static constexpr int lds(int G) { return kScales + 4 * G * (kNT + 1 + kWScales); }
-    static_assert(kNT * NW * 4 <= kRing * kStage, "the magnitudes reuse the ring");
+    static_assert(kNT * NW * 4 <= RX * kStage, "the magnitudes reuse the ring");
 };
 
 // A 16-row x 128-input piece of a row-major operand in LDS: row r's eight 16-byte chunks lie at 128 r, chunk
@@ -113,10 +113,10 @@ struct Feed {
 // The weights of a wave's rows take the way through an LDS ring of its own of RW steps: during a step's
 // last block the next step's rows have landed, and each row block's registers are read again as soon as
 // its last product is on its way; in the next step's first block the slot they left is filled again.
-template <int MODE, int RA, int NTB, int NW, int RW, int W, bool EXACT, bool TAIL>
-__device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW>::kUnits, W>& fd, uint8_t* smem, int nst,
+template <int MODE, int RA, int NTB, int NW, int RW, int RX, int W, bool EXACT, bool TAIL>
+__device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW, RX>::kUnits, W>& fd, uint8_t* smem, int nst,
                                           int K, int wv, int lane, f32x4_t (&acc)[RA][NTB]) {
-    using TL = Tile8<RA, NTB, NW, RW>;
+    using TL = Tile8<RA, NTB, NW, RW, RX>;
     constexpr int UN = TL::kUnits, WN = 2 * RA;  // token and weight loads of a step
     constexpr int MID = NTB / 2;
     constexpr int P = 4;                    // products in flight
@@ -130,7 +130,7 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW>:
     const float* xs = (const float*)(smem + TL::kScales);
     const float* ws = xs + (size_t)nst * (TL::kNT + 1);
     const int piece = lds_piece(lane);
-    uint8_t* w_area = smem + TL::kRing * TL::kStage + wv * RA * kFp8Frag;
+    uint8_t* w_area = smem + RX * TL::kStage + wv * RA * kFp8Frag;
     auto in_row = [&](int ks, int chunk) __attribute__((always_inline)) { return !TAIL || ks * 128 + 16 * chunk < K; };
     auto issue_x = [&](int ks, int slot) __attribute__((always_inline)) {
         ks = min(ks, nst - 1);  // past the end: the last stage again, into a slot nobody uses
@@ -182,7 +182,7 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW>:
     };
     int slot = 0, wslot = 0;
     auto step = [&](int ks, u32x4_t (&a)[RA][2], u32x4_t (&nxt)[RA][2]) __attribute__((always_inline)) {
-        const int next = slot + 1 < TL::kRing ? slot + 1 : 0, prev = slot >= 1 ? slot - 1 : TL::kRing - 1;
+        const int next = slot + 1 < RX ? slot + 1 : 0, prev = slot >= 1 ? slot - 1 : RX - 1;  // the slots of steps ks + 1 and ks - 1
         const int wnext = wslot + 1 < RW ? wslot + 1 : 0;
         Wide8 wide[EXACT ? RA : 1];
         if constexpr (EXACT)
@@ -212,9 +212,10 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW>:
                 issue_w(ks + RW, wslot);
             }
             if (i == RA - 1 && j == MID - 1) {
-                // the tokens of step ks + 1 have landed (younger: the weights just asked for), every wave is past step ks - 1
-                stage_barrier<WN>();
-                issue_x(ks + 2, prev);
+                // the tokens of step ks + 1 have landed (younger: the weights asked for since, and the tokens of
+                // the steps ks + 2 ..), every wave is past step ks - 1
+                stage_barrier<(RX - 2) * WN + (RX - 3) * UN>();
+                issue_x(ks + RX - 1, prev);
             }
             if (j == WJ) {
                 // the weights of step ks + 1 have landed (younger: those of ks + 2 .. ks + RW, and the tokens between)
@@ -234,13 +235,17 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW>:
 #pragma unroll
         for (int j = 0; j < NTB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    // the loads in the order in which the steps would have issued them, so that the waits' counts hold
+    // the loads in the order in which steps before the first would have issued them, so that the waits' counts hold
+    constexpr int kBefore = RW > RX - 1 ? RW : RX - 1;
 #pragma unroll
-    for (int r = 0; r < (RW > 1 ? RW - 1 : 1); ++r) issue_w(r, r);
-    issue_x(0, 0);
-    if constexpr (RW > 1) issue_w(RW - 1, RW - 1);
-    issue_x(1, 1);
-    stage_barrier<(RW > 1 ? WN : 0) + UN>();
+    for (int o = -kBefore; o < 0; ++o) {
+        if (o + RW >= 0) issue_w(o + RW, o + RW);
+        if (o + RX - 1 >= 0) issue_x(o + RX - 1, o + RX - 1);
+    }
+    // weights and tokens of step 0 have landed
+    constexpr int kAfterW = (RW - 1) * WN + (RW < RX - 1 ? RW : RX - 1) * UN;
+    constexpr int kAfterX = (RX - 2) * UN + (RW < RX - 2 ? RW : RX - 2) * WN;
+    stage_barrier<(kAfterW < kAfterX ? kAfterW : kAfterX)>();
 #pragma unroll
     for (int j = 0; j < BA; ++j) read_b(0, 0, j);
     read_s(0);
@@ -263,10 +268,10 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW>:
 }
 
 // ---- the dense product ------------------------------------------------------------------------------
-template <int RA, int NTB, int NW, int RW, bool EXACT, bool TAIL>
+template <int RA, int NTB, int NW, int RW, int RX, bool EXACT, bool TAIL>
 __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
     constexpr int W = true;
-    using TL = Tile8<RA, NTB, NW, RW>;
+    using TL = Tile8<RA, NTB, NW, RW, RX>;
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -293,7 +298,7 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
         ws[k * TL::kWScales + b] = g.w_scale[(size_t)(min(n0 + 128 * b, g.N - 1) / 128) * g.G + k];
     }
     f32x4_t acc[RA][NTB];
-    tile_loop<kDense, RA, NTB, NW, RW, kWRows, EXACT, TAIL>(fd, smem, g.G, g.K, wv, lane, acc);
+    tile_loop<kDense, RA, NTB, NW, RW, RX, kWRows, EXACT, TAIL>(fd, smem, g.G, g.K, wv, lane, acc);
 #pragma unroll
     for (int j = 0; j < NTB; ++j) {
         const int m = m0 + 16 * j + (lane & 15);
@@ -303,11 +308,11 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
     }
 }
 
-template <int RA, int NTB, int NW, int RW, bool EXACT>
+template <int RA, int NTB, int NW, int RW, int RX, bool EXACT>
 moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
-    using TL = Tile8<RA, NTB, NW, RW>;
+    using TL = Tile8<RA, NTB, NW, RW, RX>;
     const bool tail = g.K % 128 != 0;
-    auto kern = tail ? gemm_fp8_tile_kernel<RA, NTB, NW, RW, EXACT, true> : gemm_fp8_tile_kernel<RA, NTB, NW, RW, EXACT, false>;
+    auto kern = tail ? gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, EXACT, true> : gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, EXACT, false>;
     const int lds = TL::lds(g.G);
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     const dim3 grid((unsigned)((g.N + TL::kMT - 1) / TL::kMT), (unsigned)((g.M + TL::kNT - 1) / TL::kNT));
@@ -317,9 +322,9 @@ moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
 }
 
 // ---- the routed experts' projections ------------------------------------------------------------------
-template <int MODE, int RA, int NTB, int NW, int RW>
+template <int MODE, int RA, int NTB, int NW, int RW, int RX>
 __global__ __launch_bounds__(NW * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
-    using TL = Tile8<RA, NTB, NW, RW>;
+    using TL = Tile8<RA, NTB, NW, RW, RX>;
     static_assert(MODE != kGateUp || (RA % 2 == 0 && TL::kMT % 256 == 0), "gate/up tiles hold whole groups of h");
     extern __shared__ __align__(16) uint8_t smem[];
     const FfnArgs& a = p.a;
@@ -393,7 +398,7 @@ __global__ __launch_bounds__(NW * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
             ws[k * TL::kWScales + s] = ((const float*)(blk + (size_t)16 * K))[k];
         }
         f32x4_t acc[RA][NTB];
-        tile_loop<MODE, RA, NTB, NW, RW, kWFrags, false, false>(fd, smem, G, K, wv, lane, acc);
+        tile_loop<MODE, RA, NTB, NW, RW, RX, kWFrags, false, false>(fd, smem, G, K, wv, lane, acc);
         const int quad = lane >> 4;
         if constexpr (MODE == kGateUp) {
             constexpr int GW = 16 / RA;  // waves that share a 128-column group of h
@@ -444,13 +449,13 @@ __global__ __launch_bounds__(NW * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
     }
 }
 
-template <int MODE, int RA, int NTB, int NW, int RW>
+template <int MODE, int RA, int NTB, int NW, int RW, int RX>
 moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
-    using TL = Tile8<RA, NTB, NW, RW>;
+    using TL = Tile8<RA, NTB, NW, RW, RX>;
     const int64_t items = work_items(p.a, TL::kNT);
     if (items <= 0) return MOE_OK;
     const int nblk = MODE == kGateUp ? 2 * (p.a.f / 16) : p.a.d / 16;
-    auto kern = ffn_fp8_tile_kernel<MODE, RA, NTB, NW, RW>;
+    auto kern = ffn_fp8_tile_kernel<MODE, RA, NTB, NW, RW, RX>;
     const int lds = TL::lds((MODE == kGateUp ? p.a.d : p.a.f) / 128);
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     ProfScope sc(name, st);
@@ -462,13 +467,50 @@ moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
 
 }  // namespace
 
-// MOE_EDTYPE where the tiles do not apply
-moe_status gemm_fp8_tile(const GemmFp8& g, hipStream_t st) {
-    if (g.G > 192 || g.ldw > (1u << 22) || g.M > 65535 * 32) return MOE_EDTYPE;  // scales fit LDS, offsets 32 bits
-    // fewer tiles than half the compute units: the streaming kernel splits the work finer
-    if ((int64_t)((g.N + 511) / 512) * ((g.M + 127) / 128) < 128) return MOE_EDTYPE;
-    if (!g.c_bf16) return launch_gemm<2, 8, 8, 2, true>(g, st);
-    return launch_gemm<4, 8, 8, 1, false>(g, st);
+// The tiles, and what a 128-input step of one costs (us): alone on a compute unit, and where every unit
+// has a full share of them.  Measured on 32-step products of 256 to 8192 rows; a product's time follows as
+// 3 us + steps * max(alone, rounds * full) to within 15 % over 64 .. 8192 rows and 512 .. 8192 columns.
+// Large tiles read less from LDS a product, small ones fill the chip with fewer rows.
+namespace {
+struct TileCost {
+    int mt, nt;
+    float alone, full;
+    int (*lds)(int G);
+    moe_status (*launch)(const GemmFp8&, hipStream_t);
+};
+template <int RA, int NTB, int NW, int RW, int RX, bool EXACT>
+constexpr TileCost cost(float alone, float full) {
+    using TL = Tile8<RA, NTB, NW, RW, RX>;
+    return {TL::kMT, TL::kNT, alone, full, TL::lds, launch_gemm<RA, NTB, NW, RW, RX, EXACT>};
+}
+constexpr TileCost kTiles[] = {
+    cost<4, 8, 8, 1, 3, false>(1.70f, 2.10f), cost<2, 8, 8, 2, 3, false>(0.99f, 1.27f),
+    cost<2, 4, 8, 2, 4, false>(0.66f, 0.74f), cost<2, 4, 4, 2, 4, false>(0.49f, 0.36f),
+    cost<1, 4, 4, 2, 4, false>(0.39f, 0.255f)};
+constexpr TileCost kExactTiles[] = {cost<2, 8, 8, 1, 4, true>(1.70f, 2.04f), cost<2, 4, 4, 3, 5, true>(0.75f, 0.78f),
+                                    cost<1, 4, 4, 3, 5, true>(0.60f, 0.45f)};
+}  // namespace
+
+const void* gemm_fp8_best_tile(const GemmFp8& g, float& us) {
+    const TileCost* best = nullptr;
+    us = 0.f;
+    if (g.ldw > (1u << 22)) return nullptr;  // a tile's weight offsets have 32 bits
+    auto look = [&](const TileCost& t) {
+        const int64_t rows = (g.M + t.nt - 1) / t.nt, tiles = (int64_t)((g.N + t.mt - 1) / t.mt) * rows;
+        if (t.lds(g.G) > kLds || rows > 65535) return;
+        const float rounds = (float)((tiles + kCUs - 1) / kCUs);
+        const float e = 3.0f + g.G * std::max(t.alone, rounds * t.full);
+        if (!best || e < us) best = &t, us = e;
+    };
+    if (g.c_bf16)
+        for (const TileCost& t : kTiles) look(t);
+    else
+        for (const TileCost& t : kExactTiles) look(t);
+    return best;
+}
+
+moe_status gemm_fp8_tile(const GemmFp8& g, const void* tile, hipStream_t st) {
+    return ((const TileCost*)tile)->launch(g, st);
 }
 
 #ifndef TILE_SPLIT
@@ -476,19 +518,19 @@ moe_status gemm_fp8_tile(const GemmFp8& g, hipStream_t st) {
 #endif
 moe_status ffn_fp8_tile(const FfnFp8& p, int mode, hipStream_t st) {
     const int G = (mode == kGateUp ? p.a.d : p.a.f) / 128;
-    if (p.a.T <= 64 || Tile8<4, 8, 8, 1>::lds(G) > kLds) {  // at most 64 tokens an expert, or too many scales for the LDS
-        return mode == kGateUp ? launch_ffn<kGateUp, 2, 4, 8, 3>(p, st, "ffn_fp8_gateup_tile_light")
-                               : launch_ffn<kDown, 2, 4, 8, 3>(p, st, "ffn_fp8_down_tile_light");
+    if (p.a.T <= 64 || Tile8<4, 8, 8, 1, 3>::lds(G) > kLds) {  // at most 64 tokens an expert, or too many scales for the LDS
+        return mode == kGateUp ? launch_ffn<kGateUp, 2, 4, 8, 3, 4>(p, st, "ffn_fp8_gateup_tile_light")
+                               : launch_ffn<kDown, 2, 4, 8, 3, 4>(p, st, "ffn_fp8_down_tile_light");
     }
     FfnFp8 heavy = p, light = p;
     heavy.a.n_lo = TILE_SPLIT + 1;
     light.a.n_hi = TILE_SPLIT;
     if (mode == kGateUp) {
-        moe_status r = launch_ffn<kGateUp, 4, 8, 8, 1>(heavy, st, "ffn_fp8_gateup_tile");
-        return r != MOE_OK ? r : launch_ffn<kGateUp, 2, 4, 8, 3>(light, st, "ffn_fp8_gateup_tile_light");
+        moe_status r = launch_ffn<kGateUp, 4, 8, 8, 1, 3>(heavy, st, "ffn_fp8_gateup_tile");
+        return r != MOE_OK ? r : launch_ffn<kGateUp, 2, 4, 8, 3, 4>(light, st, "ffn_fp8_gateup_tile_light");
     }
-    moe_status r = launch_ffn<kDown, 4, 8, 8, 1>(heavy, st, "ffn_fp8_down_tile");
-    return r != MOE_OK ? r : launch_ffn<kDown, 2, 4, 8, 3>(light, st, "ffn_fp8_down_tile_light");
+    moe_status r = launch_ffn<kDown, 4, 8, 8, 1, 3>(heavy, st, "ffn_fp8_down_tile");
+    return r != MOE_OK ? r : launch_ffn<kDown, 2, 4, 8, 3, 4>(light, st, "ffn_fp8_down_tile_light");
 }
 
 }  // namespace moe
