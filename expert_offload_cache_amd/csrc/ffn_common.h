@@ -195,19 +195,24 @@ __device__ __forceinline__ bool find_work_slot(const int32_t* __restrict__ count
 }
 
 // Work item `a` of a launch -> (expert, chunk, slot, tokens of the expert, its first sorted row):
-// find_work_slot where a lane covers at most 4 experts (E <= 256), else find_work and then the
+// over the experts with n_lo to n_hi tokens (the launch's, if not given); find_work_slot where a lane
+// covers at most 4 experts (E <= 256), else find_work and then the
 // expert's slot, count and offset.
 __device__ __forceinline__ bool find_item(const FfnArgs& f, int ntg, int a, int& e, int& chunk, int& slot, int& n,
-                                          int& p0) {
+                                          int& p0, int n_lo, int n_hi) {
     if (f.E <= 256)
         return find_work_slot<4>(f.counts, f.slot_of_expert, f.E, f.T, f.k, ntg, f.shared_w != nullptr, a, e, chunk,
-                                 slot, n, p0, f.n_lo, f.n_hi);
-    if (!find_work(f.counts, f.E, f.T, ntg, f.shared_w != nullptr, a, e, chunk, f.n_lo, f.n_hi)) return false;
+                                 slot, n, p0, n_lo, n_hi);
+    if (!find_work(f.counts, f.E, f.T, ntg, f.shared_w != nullptr, a, e, chunk, n_lo, n_hi)) return false;
     const bool shared = e == -1;
     slot = shared ? -1 : __builtin_amdgcn_readfirstlane(f.slot_of_expert[e]);
     n = __builtin_amdgcn_readfirstlane(shared ? f.T : f.counts[e]);
     p0 = __builtin_amdgcn_readfirstlane(shared ? f.T * f.k : f.offsets[e]);
     return true;
+}
+__device__ __forceinline__ bool find_item(const FfnArgs& f, int ntg, int a, int& e, int& chunk, int& slot, int& n,
+                                          int& p0) {
+    return find_item(f, ntg, a, e, chunk, slot, n, p0, f.n_lo, f.n_hi);
 }
 
 template <int W>

@@ -113,9 +113,10 @@ struct Feed {
 // The weights of a wave's rows take the way through an LDS ring of its own of RW steps: during a step's
 // last block the next step's rows have landed, and each row block's registers are read again as soon as
 // its last product is on its way; in the next step's first block the slot they left is filled again.
-template <int MODE, int RA, int NTB, int NW, int RW, int RX, int W, bool EXACT, bool TAIL>
+template <int MODE, int RA, int NTB, int NW, int RW, int RX, int W, bool EXACT, bool TAIL, typename SX, typename SW>
 __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW, RX>::kUnits, W>& fd, uint8_t* smem, int nst,
-                                          int K, int wv, int lane, f32x4_t (&acc)[RA][NTB]) {
+                                          int K, int wv, int lane, int tid, SX&& x_scales, SW&& w_scales,
+                                          f32x4_t (&acc)[RA][NTB]) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     constexpr int UN = TL::kUnits, WN = 2 * RA;  // token and weight loads of a step
     constexpr int MID = NTB / 2;
@@ -242,6 +243,22 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW, 
         if (o + RW >= 0) issue_w(o + RW, o + RW);
         if (o + RX - 1 >= 0) issue_x(o + RX - 1, o + RX - 1);
     }
+    // Meanwhile the scales of the whole tile: thread t those of token t % NT, every (threads / NT)-th
+    // step (x_scales(token): its row of scales), then of the weights' 128-row blocks (w_scales(block)).
+    {
+        constexpr int PER = NW * 64 / TL::kNT;
+        static_assert(PER * TL::kNT == NW * 64, "threads divide over the tokens");
+        float* to = (float*)(smem + TL::kScales);
+        const int t = tid % TL::kNT;
+        const float* from = x_scales(t);
+#pragma unroll 8
+        for (int k = tid / TL::kNT; k < nst; k += PER) to[k * (TL::kNT + 1) + t] = from[k];
+        to += (size_t)nst * (TL::kNT + 1);
+        for (int i = tid; i < nst * TL::kWScales; i += NW * 64) {
+            const int b = i / nst, k = i - b * nst;
+            to[k * TL::kWScales + b] = w_scales(b)[k];
+        }
+    }
     // weights and tokens of step 0 have landed
     constexpr int kAfterW = (RW - 1) * WN + (RW < RX - 1 ? RW : RX - 1) * UN;
     constexpr int kAfterX = (RX - 2) * UN + (RW < RX - 2 ? RW : RX - 2) * WN;
@@ -287,18 +304,10 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
         const int m = min(m0 + 8 * (wv * TL::kUnits + u) + (lane >> 3), g.M - 1);
         fd.x[u] = g.a + (size_t)m * g.lda + 16 * chunk_of_lane(lane);
     }
-    float* xs = (float*)(smem + TL::kScales);
-    float* ws = xs + (size_t)g.G * (TL::kNT + 1);
-    for (int i = threadIdx.x; i < g.G * TL::kNT; i += NW * 64) {
-        const int t = i / g.G, k = i - t * g.G;
-        xs[k * (TL::kNT + 1) + t] = g.a_scale[(size_t)min(m0 + t, g.M - 1) * g.G + k];
-    }
-    for (int i = threadIdx.x; i < g.G * TL::kWScales; i += NW * 64) {
-        const int b = i / g.G, k = i - b * g.G;
-        ws[k * TL::kWScales + b] = g.w_scale[(size_t)(min(n0 + 128 * b, g.N - 1) / 128) * g.G + k];
-    }
     f32x4_t acc[RA][NTB];
-    tile_loop<kDense, RA, NTB, NW, RW, RX, kWRows, EXACT, TAIL>(fd, smem, g.G, g.K, wv, lane, acc);
+    tile_loop<kDense, RA, NTB, NW, RW, RX, kWRows, EXACT, TAIL>(
+        fd, smem, g.G, g.K, wv, lane, threadIdx.x, [&](int t) { return g.a_scale + (size_t)min(m0 + t, g.M - 1) * g.G; },
+        [&](int b) { return g.w_scale + (size_t)(min(n0 + 128 * b, g.N - 1) / 128) * g.G; }, acc);
 #pragma unroll
     for (int j = 0; j < NTB; ++j) {
         const int m = m0 + 16 * j + (lane & 15);
@@ -322,36 +331,40 @@ moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
 }
 
 // ---- the routed experts' projections ------------------------------------------------------------------
+// The chunks of nt tokens of the experts that hold n_lo to n_hi (every lane gets the sum).
+__device__ __forceinline__ int count_chunks(const FfnArgs& a, int nt, int n_lo, int n_hi) {
+    auto chunks = [&](int n) { return n >= n_lo && n <= n_hi ? (n + nt - 1) / nt : 0; };
+    int c = 0;
+    for (int e = threadIdx.x & 63; e < a.E; e += 64) c += chunks(a.counts[e]);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) c += __shfl_xor(c, s, 64);
+    return __builtin_amdgcn_readfirstlane(c) + (a.shared_w ? chunks(a.T) : 0);
+}
+
+// This workgroup's tiles (first, first + gridDim.x, ...) of the experts that hold n_lo to n_hi tokens.
 template <int MODE, int RA, int NTB, int NW, int RW, int RX>
-__global__ __launch_bounds__(NW * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
+__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_lo, int n_hi, int64_t first) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     static_assert(MODE != kGateUp || (RA % 2 == 0 && TL::kMT % 256 == 0), "gate/up tiles hold whole groups of h");
-    extern __shared__ __align__(16) uint8_t smem[];
     const FfnArgs& a = p.a;
     const int nblk = MODE == kGateUp ? 2 * (a.f / 16) : a.d / 16;
     const int gx = (nblk + NW * RA - 1) / (NW * RA);  // tiles over the weight rows
-    // The grid is at most one workgroup for each that can run at once; each takes every gridDim.x-th
-    // tile, until the work items that the counts give are through (a launch without any ends at once:
-    // 19 and 58 us with a grid for the most there could be).
-    for (int64_t id = blockIdx.x;; id += gridDim.x) {
+    for (int64_t id = first;; id += gridDim.x) {
         // The empty asm statements make these values new in each pass: otherwise everything that depends on
         // them alone is computed before the loop and held in registers across it, which spills.
         int tid = threadIdx.x, K = MODE == kGateUp ? a.d : a.f;
         asm volatile("" : "+v"(tid), "+s"(K));
         const int lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), G = K / 128;
         const int bx = (int)(id % gx);
-        int e, chunk;
-        if (!find_work(a.counts, a.E, a.T, TL::kNT, a.shared_w != nullptr, (int)(id / gx), e, chunk, a.n_lo, a.n_hi)) return;
+        int e, chunk, slot, n_all, p0;
+        if (!find_item(a, TL::kNT, (int)(id / gx), e, chunk, slot, n_all, p0, n_lo, n_hi)) return;
         const bool shared = e == -1;
-        const int n_all = __builtin_amdgcn_readfirstlane(shared ? a.T : a.counts[e]);
-        const int t0 = chunk * TL::kNT;
-        const int nt = __builtin_amdgcn_readfirstlane(min(TL::kNT, n_all - t0));
-        const int p0 = __builtin_amdgcn_readfirstlane(shared ? a.T * a.k : a.offsets[e]) + t0;  // first row of the tile
+        const int nt = min(TL::kNT, n_all - chunk * TL::kNT);
+        p0 += chunk * TL::kNT;  // first row of the tile
         const uint8_t* base;
         if (shared) {
             base = a.shared_w;
         } else {
-            const int slot = __builtin_amdgcn_readfirstlane(a.slot_of_expert[e]);
             if (slot == MOE_SLOT_ELSEWHERE) continue;  // rows produced elsewhere: leave them
             if (slot < 0 || slot >= a.n_slots) {     // absent: flagged, zero rows (h is not read then)
                 if (tid == 0) *a.status = 1;
@@ -384,21 +397,16 @@ __global__ __launch_bounds__(NW * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
 #pragma unroll
         for (int u = 0; u < TL::kUnits; ++u)
             fd.x[u] = x + (size_t)source(8 * (wv * TL::kUnits + u) + (lane >> 3)) * K + 16 * chunk_of_lane(lane);
-        float* xs = (float*)(smem + TL::kScales);
-        float* ws = xs + (size_t)G * (TL::kNT + 1);
-        for (int i = tid; i < G * TL::kNT; i += NW * 64) {
-            const int t = i / G, k = i - t * G;
-            xs[k * (TL::kNT + 1) + t] = x_scale[(size_t)source(t) * G + k];
-        }
-        for (int i = tid; i < G * TL::kWScales; i += NW * 64) {
-            const int s = i / G, k = i - s * G;
-            // gate/up: the gate and the up scale of each 128 columns of h (16 blocks); down: of 8 blocks
-            const int b = min(bw + (MODE == kGateUp ? 16 * (s >> 1) + (s & 1) : 8 * s), nblk - 2 + (MODE == kGateUp ? (s & 1) : 1));
-            const uint8_t* blk = base + (MODE == kGateUp ? 0 : down_block_offset(0, a.d, a.f, MOE_FP8_B128)) + (size_t)b * rbb;
-            ws[k * TL::kWScales + s] = ((const float*)(blk + (size_t)16 * K))[k];
-        }
         f32x4_t acc[RA][NTB];
-        tile_loop<MODE, RA, NTB, NW, RW, RX, kWFrags, false, false>(fd, smem, G, K, wv, lane, acc);
+        tile_loop<MODE, RA, NTB, NW, RW, RX, kWFrags, false, false>(
+            fd, smem, G, K, wv, lane, tid, [&](int t) { return x_scale + (size_t)source(t) * G; },
+            [&](int s) {
+                // gate/up: the gate and the up scale of each 128 columns of h (16 blocks); down: of 8 blocks
+                const int b = min(bw + (MODE == kGateUp ? 16 * (s >> 1) + (s & 1) : 8 * s),
+                                  nblk - 2 + (MODE == kGateUp ? (s & 1) : 1));
+                return (const float*)(fd.w + (size_t)(b - bw) * rbb + (size_t)16 * K);
+            },
+            acc);
         const int quad = lane >> 4;
         if constexpr (MODE == kGateUp) {
             constexpr int GW = 16 / RA;  // waves that share a 128-column group of h
@@ -449,19 +457,45 @@ __global__ __launch_bounds__(NW * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
     }
 }
 
-template <int MODE, int RA, int NTB, int NW, int RW, int RX>
+// Experts with up to kLight tokens take 256-row x 64-token tiles, with the weights two steps ahead: their
+// weights' bytes bound them.  The others take 512 x 128, or 256 x 128 where that still leaves every
+// tile a compute unit of its own (517 tokens on 8 of 128 experts: LIGHT_GAIN).  HEAVY false: no expert of
+// the call can hold more, or the larger tiles' scales exceed the LDS (inputs beyond 11776).
+constexpr int kLight = 64, kMost = 1 << 30, kWaves = 8;
+typedef Tile8<4, 8, kWaves, 1, 3> TileLarge;
+typedef Tile8<2, 8, kWaves, 2, 3> TileMid;
+typedef Tile8<2, 4, kWaves, 2, 4> TileLight;
+
+// The grid is at most one workgroup a compute unit; each takes every gridDim.x-th tile until the work that
+// the counts give is through (a launch for the most there could be took 19 to 58 us to find nothing).
+template <int MODE, bool HEAVY>
+__global__ __launch_bounds__(kWaves * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    int64_t first = blockIdx.x;
+    if constexpr (HEAVY) {
+        const int64_t rows = MODE == kGateUp ? 2 * p.a.f : p.a.d, chunks = count_chunks(p.a, TileLarge::kNT, kLight + 1, kMost);
+        int64_t tiles = chunks * ((rows + TileLarge::kMT - 1) / TileLarge::kMT);
+        if (tiles > kCUs / 2) {
+            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, smem, kLight + 1, kMost, first);
+        } else {
+            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, smem, kLight + 1, kMost, first);
+            tiles = chunks * ((rows + TileMid::kMT - 1) / TileMid::kMT);
+        }
+        // the light tiles begin with the workgroup that the heavy ones' last round did not reach
+        first = (blockIdx.x + gridDim.x - tiles % gridDim.x) % gridDim.x;
+    }
+    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, smem, 0, HEAVY ? kLight : kMost, first);
+}
+
+template <int MODE, bool HEAVY>
 moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
-    using TL = Tile8<RA, NTB, NW, RW, RX>;
-    const int64_t items = work_items(p.a, TL::kNT);
-    if (items <= 0) return MOE_OK;
-    const int nblk = MODE == kGateUp ? 2 * (p.a.f / 16) : p.a.d / 16;
-    auto kern = ffn_fp8_tile_kernel<MODE, RA, NTB, NW, RW, RX>;
-    const int lds = TL::lds((MODE == kGateUp ? p.a.d : p.a.f) / 128);
+    const int G = (MODE == kGateUp ? p.a.d : p.a.f) / 128, rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
+    const int lds = HEAVY ? std::max(TileLight::lds(G), std::max(TileLarge::lds(G), TileMid::lds(G))) : TileLight::lds(G);
+    auto kern = ffn_fp8_tile_kernel<MODE, HEAVY>;
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+    const int64_t tiles = work_items(p.a, TileLight::kNT) * ((rows + TileLight::kMT - 1) / TileLight::kMT);
     ProfScope sc(name, st);
-    const int64_t tiles = items * ((nblk + NW * RA - 1) / (NW * RA));
-    const int64_t resident = (int64_t)kCUs * std::max(1, std::min(kLds / lds, 16 / NW));
-    kern<<<(unsigned)std::min(tiles, resident), NW * 64, lds, st>>>(p);
+    kern<<<(unsigned)std::min<int64_t>(tiles, kCUs), kWaves * 64, lds, st>>>(p);
     return check_launch(name);
 }
 
@@ -513,24 +547,13 @@ moe_status gemm_fp8_tile(const GemmFp8& g, const void* tile, hipStream_t st) {
     return ((const TileCost*)tile)->launch(g, st);
 }
 
-#ifndef TILE_SPLIT
-#define TILE_SPLIT 64
-#endif
 moe_status ffn_fp8_tile(const FfnFp8& p, int mode, hipStream_t st) {
     const int G = (mode == kGateUp ? p.a.d : p.a.f) / 128;
-    if (p.a.T <= 64 || Tile8<4, 8, 8, 1, 3>::lds(G) > kLds) {  // at most 64 tokens an expert, or too many scales for the LDS
-        return mode == kGateUp ? launch_ffn<kGateUp, 2, 4, 8, 3, 4>(p, st, "ffn_fp8_gateup_tile_light")
-                               : launch_ffn<kDown, 2, 4, 8, 3, 4>(p, st, "ffn_fp8_down_tile_light");
-    }
-    FfnFp8 heavy = p, light = p;
-    heavy.a.n_lo = TILE_SPLIT + 1;
-    light.a.n_hi = TILE_SPLIT;
-    if (mode == kGateUp) {
-        moe_status r = launch_ffn<kGateUp, 4, 8, 8, 1, 3>(heavy, st, "ffn_fp8_gateup_tile");
-        return r != MOE_OK ? r : launch_ffn<kGateUp, 2, 4, 8, 3, 4>(light, st, "ffn_fp8_gateup_tile_light");
-    }
-    moe_status r = launch_ffn<kDown, 4, 8, 8, 1, 3>(heavy, st, "ffn_fp8_down_tile");
-    return r != MOE_OK ? r : launch_ffn<kDown, 2, 4, 8, 3, 4>(light, st, "ffn_fp8_down_tile_light");
+    const bool heavy = p.a.T > kLight && TileLarge::lds(G) <= kLds && TileMid::lds(G) <= kLds;
+    if (mode == kGateUp)
+        return heavy ? launch_ffn<kGateUp, true>(p, st, "ffn_fp8_gateup_tile")
+                     : launch_ffn<kGateUp, false>(p, st, "ffn_fp8_gateup_tile");
+    return heavy ? launch_ffn<kDown, true>(p, st, "ffn_fp8_down_tile") : launch_ffn<kDown, false>(p, st, "ffn_fp8_down_tile");
 }
 
 }  // namespace moe
