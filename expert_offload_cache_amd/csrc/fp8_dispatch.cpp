@@ -72,7 +72,7 @@ moe_status moe_gemm_fp8(const void* a, size_t lda, const float* a_scale, int M, 
     g.K = K;
     g.G = fp8_groups(K);
     g.c_bf16 = out == MOE_BF16;
-    g.c_vec = (uintptr_t)c % (4 * esz) == 0 && ldc % 4 == 0;
+    g.c_vec = (uintptr_t)c % 16 == 0 && ldc * esz % 16 == 0;
     float tile_us;
     const void* tile = gemm_fp8_best_tile(g, tile_us);
     if (tile && tile_us < gemm_fp8_stream_us(g)) return gemm_fp8_tile(g, tile, (hipStream_t)s);

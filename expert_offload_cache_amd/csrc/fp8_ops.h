@@ -19,7 +19,7 @@ struct GemmFp8 {
     size_t ldc;
     int M, N, K, G;
     int c_bf16;  // c elements: bf16 (each sum rounded once), else binary32
-    int c_vec;   // four consecutive elements of c may be stored at once
+    int c_vec;   // rows of c start on 16 bytes
 };
 
 // four consecutive columns n .. of row m of c

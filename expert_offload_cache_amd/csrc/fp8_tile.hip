@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ffn_common.h"
 #include "fp8_ops.h"
@@ -243,16 +244,15 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW, 
         if (o + RW >= 0) issue_w(o + RW, o + RW);
         if (o + RX - 1 >= 0) issue_x(o + RX - 1, o + RX - 1);
     }
-    // Meanwhile the scales of the whole tile: thread t those of token t % NT, every (threads / NT)-th
-    // step (x_scales(token): its row of scales), then of the weights' 128-row blocks (w_scales(block)).
+    // Meanwhile the scales of the whole tile: the tokens' (x_scales(token): its row of scales), then
+    // those of the weights' 128-row blocks (w_scales(block)).
     {
-        constexpr int PER = NW * 64 / TL::kNT;
-        static_assert(PER * TL::kNT == NW * 64, "threads divide over the tokens");
         float* to = (float*)(smem + TL::kScales);
-        const int t = tid % TL::kNT;
-        const float* from = x_scales(t);
-#pragma unroll 8
-        for (int k = tid / TL::kNT; k < nst; k += PER) to[k * (TL::kNT + 1) + t] = from[k];
+#pragma unroll 4
+        for (int i = tid; i < nst * TL::kNT; i += NW * 64) {
+            const int t = i / nst, k = i - t * nst;
+            to[k * (TL::kNT + 1) + t] = x_scales(t)[k];
+        }
         to += (size_t)nst * (TL::kNT + 1);
         for (int i = tid; i < nst * TL::kWScales; i += NW * 64) {
             const int b = i / nst, k = i - b * nst;
@@ -284,11 +284,59 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW, 
     stage_barrier<0>();  // the tail's repeated loads have landed, every wave has left the ring
 }
 
+// A wave's sums (RA * 16 columns x NTB * 16 tokens) to rows of E (bf16 or binary32), through LDS so that a
+// store takes whole pieces of rows: 1 KB of 16-byte chunks a wave instead of 16 rows x 32 bytes.  area: 8 KB of
+// the wave's own.  row(t): where token t's columns begin, nullptr to leave them; cols of them exist; wide:
+// rows start on 16 bytes.  Chunk c of token t lies at position c ^ (t mod chunks of a row).
+template <typename E, int RA, int NTB, typename Row>
+__device__ __forceinline__ void store_rows(const f32x4_t (&acc)[RA][NTB], uint8_t* area, int lane, int cols, bool wide,
+                                           Row&& row) {
+    constexpr int BYTES = RA * 16 * sizeof(E), CH = BYTES / 16, PER = 16 / sizeof(E);  // of a token; elements a chunk
+    constexpr int JP = 8192 / (16 * BYTES) < NTB ? 8192 / (16 * BYTES) : NTB;            // token blocks a pass
+    const int q = lane >> 4;
+#pragma unroll
+    for (int j0 = 0; j0 < NTB; j0 += JP) {
+        wait_lds();  // the pass before has been read
+#pragma unroll
+        for (int j = j0; j < j0 + JP; ++j) {
+            const int t = 16 * (j - j0) + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < RA; ++i) {
+                const f32x4_t v = acc[i][j];
+                if constexpr (sizeof(E) == 2) {
+                    uint2 o;
+                    o.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
+                    o.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
+                    *(uint2*)(area + t * BYTES + (((2 * i + (q >> 1)) ^ (t & (CH - 1))) << 4) + 8 * (q & 1)) = o;
+                } else {
+                    *(float4*)(area + t * BYTES + (((4 * i + q) ^ (t & (CH - 1))) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+        wait_lds();
+        if (wide && cols >= RA * 16) {
+            for (int i = lane; i < JP * 16 * CH; i += 64) {
+                const int t = i / CH, c = i % CH;
+                E* to = row(16 * j0 + t);
+                if (to) *(u32x4_t*)(to + c * PER) = *(const u32x4_t*)(area + t * BYTES + ((c ^ (t & (CH - 1))) << 4));
+            }
+        } else {  // element by element, neighbouring lanes neighbouring columns
+            for (int i = lane; i < JP * 16 * RA * 16; i += 64) {
+                const int t = i / (RA * 16), c = i % (RA * 16);
+                E* to = row(16 * j0 + t);
+                if (to && c < cols)
+                    to[c] = *(const E*)(area + t * BYTES + (((c / PER) ^ (t & (CH - 1))) << 4) + (c % PER) * sizeof(E));
+            }
+        }
+    }
+}
+
 // ---- the dense product ------------------------------------------------------------------------------
 template <int RA, int NTB, int NW, int RW, int RX, bool EXACT, bool TAIL>
 __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
     constexpr int W = true;
     using TL = Tile8<RA, NTB, NW, RW, RX>;
+    typedef std::conditional_t<EXACT, float, uint16_t> OutT;  // binary32 results are the exact ones
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -308,13 +356,13 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
     tile_loop<kDense, RA, NTB, NW, RW, RX, kWRows, EXACT, TAIL>(
         fd, smem, g.G, g.K, wv, lane, threadIdx.x, [&](int t) { return g.a_scale + (size_t)min(m0 + t, g.M - 1) * g.G; },
         [&](int b) { return g.w_scale + (size_t)(min(n0 + 128 * b, g.N - 1) / 128) * g.G; }, acc);
-#pragma unroll
-    for (int j = 0; j < NTB; ++j) {
-        const int m = m0 + 16 * j + (lane & 15);
-        if (m >= g.M) continue;
-#pragma unroll
-        for (int i = 0; i < RA; ++i) store_c4(g, m, nrow + 16 * i + 4 * (lane >> 4), acc[i][j]);
-    }
+    // the ring is free: every wave has left it
+    static_assert(NW * 8192 <= RX * TL::kStage + RW * TL::kWBytes, "the waves' 8 KB");
+    uint8_t* area = smem + wv * 8192;
+    auto row = [&](int t) __attribute__((always_inline)) {
+        return m0 + t < g.M ? (OutT*)g.c + (size_t)(m0 + t) * g.ldc + nrow : nullptr;
+    };
+    store_rows<OutT>(acc, area, lane, g.N - nrow, g.c_vec, row);
 }
 
 template <int RA, int NTB, int NW, int RW, int RX, bool EXACT>
@@ -426,32 +474,44 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_
                 if (quad == 0) mags[wv * TL::kNT + 16 * j + lane] = m;
             }
             __syncthreads();
-            const int col0 = b0 / 2 * 16;
+            // h in 8 bits, all of the tile's columns of a token side by side in LDS (16-byte chunk c at c ^ (t mod 16)),
+            // then out in whole pieces of rows
+            constexpr int COLS = TL::kMT / 2, CH = COLS / 16;
+            static_assert((NW + COLS / 4) * TL::kNT * 4 <= RX * TL::kStage + RW * TL::kWBytes, "magnitudes and h");
+            uint8_t* tile = smem + NW * TL::kNT * 4;
+            const int cw = wv * RA * 8;  // this wave's first column of the tile
 #pragma unroll
             for (int j = 0; j < NTB; ++j) {
                 const int t = 16 * j + (lane & 15);
-                if (t >= nt || b0 >= nblk) continue;
                 uint32_t m = 0;
 #pragma unroll
                 for (int w = 0; w < GW; ++w) m = umax(m, mags[(wv / GW * GW + w) * TL::kNT + t]);
                 const float s = fp8_scale(m), r = 1.0f / s;
-                const size_t row = (size_t)(p0 + t);
 #pragma unroll
                 for (int i = 0; i < RA / 2; ++i)
-                    *(uint32_t*)(p.h8 + row * a.f + col0 + 16 * i + 4 * quad) =
+                    *(uint32_t*)(tile + t * COLS + ((((cw >> 4) + i) ^ (t & (CH - 1))) << 4) + 4 * quad) =
                         fp8_pack4(acc[2 * i][j][0], acc[2 * i][j][1], acc[2 * i][j][2], acc[2 * i][j][3], r);
-                if (wv % GW == 0 && quad == 0) p.h_scale[row * (a.f / 128) + col0 / 128] = s;
+                const int c = bx * COLS + cw;
+                if (wv % GW == 0 && quad == 0 && t < nt && c < a.f) p.h_scale[(size_t)(p0 + t) * (a.f / 128) + c / 128] = s;
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NTB; ++j) {
-                const int t = 16 * j + (lane & 15);
-                if (t >= nt || b0 >= nblk) continue;
-#pragma unroll
-                for (int i = 0; i < RA; ++i)
-                    store_y4(a, (size_t)(p0 + t), (b0 + i) * 16 + 4 * quad, acc[i][j][0], acc[i][j][1], acc[i][j][2],
-                             acc[i][j][3]);
+            __syncthreads();
+            for (int i = tid; i < nt * CH; i += NW * 64) {
+                const int t = i / CH, c = i % CH, col = bx * COLS + 16 * c;
+                if (col < a.f)
+                    *(u32x4_t*)(p.h8 + (size_t)(p0 + t) * a.f + col) = *(const u32x4_t*)(tile + t * COLS + ((c ^ (t & (CH - 1))) << 4));
             }
+        } else if (b0 < nblk) {
+            static_assert(NW * 8192 <= RX * TL::kStage + RW * TL::kWBytes, "the waves' 8 KB");
+            uint8_t* area = smem + wv * 8192;
+            auto rows = [&](auto* y) __attribute__((always_inline)) {
+                typedef std::remove_pointer_t<decltype(y)> E;
+                auto row = [&](int t) __attribute__((always_inline)) {
+                    return t < nt ? y + (size_t)(p0 + t) * a.d + b0 * 16 : nullptr;
+                };
+                store_rows<E>(acc, area, lane, RA * 16, true, row);
+            };
+            if (a.y_bf16) rows((uint16_t*)a.y_perm);
+            else rows((float*)a.y_perm);
         }
         __syncthreads();  // the next tile's scales and magnitudes take the same LDS
     }
