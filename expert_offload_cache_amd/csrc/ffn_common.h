@@ -194,10 +194,9 @@ __device__ __forceinline__ bool find_work_slot(const int32_t* __restrict__ count
     return true;
 }
 
-// Work item `a` of a launch -> (expert, chunk, slot, tokens of the expert, its first sorted row):
-// over the experts with n_lo to n_hi tokens (the launch's, if not given); find_work_slot where a lane
-// covers at most 4 experts (E <= 256), else find_work and then the
-// expert's slot, count and offset.
+// Work item `a` of a launch -> (expert, chunk, slot, tokens of the expert, its first sorted row), over
+// the experts with n_lo to n_hi tokens (the launch's, if not given): find_work_slot where a lane covers
+// at most 4 experts (E <= 256), else find_work and then the expert's slot, count and offset.
 __device__ __forceinline__ bool find_item(const FfnArgs& f, int ntg, int a, int& e, int& chunk, int& slot, int& n,
                                           int& p0, int n_lo, int n_hi) {
     if (f.E <= 256)

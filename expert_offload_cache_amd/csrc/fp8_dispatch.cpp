@@ -1,6 +1,8 @@
 // moe_gemm_fp8 and moe_expert_ffn_fp8: argument checks and the choice of kernel.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "fp8_ops.h"
 #include "slot_layout.h"
 
@@ -11,10 +13,13 @@ namespace moe {
 // n rows of w e4m3 values and their scales behind them
 static size_t rows8_bytes(size_t n, int w) { return align_up(n * w, 256) + align_up(n * (w / 128) * 4, 256); }
 
+// h of the streaming kernels, or x and h in 8 bits; never less than fewer tokens take, so that a workspace of the
+// most tokens serves every call
 size_t ffn_fp8_workspace(int T, int d, int f, int k, int has_shared) {
-    const size_t rows = (size_t)T * k + (has_shared ? (size_t)T : 0);
-    return kWsHeader + kPlanBytes +
-           (T <= kFp8Stream ? align_up(rows * f * 4, 256) : rows8_bytes(T, d) + rows8_bytes(rows, f));
+    const size_t per = (size_t)k + (has_shared ? 1 : 0);
+    const size_t few = align_up(std::min(T, kFp8Stream) * per * f * 4, 256);
+    const size_t many = T > kFp8Stream ? rows8_bytes(T, d) + rows8_bytes(T * per, f) : 0;
+    return kWsHeader + kPlanBytes + std::max(few, many);
 }
 
 moe_status ffn_fp8_run(const FfnFp8& call, hipStream_t st) {

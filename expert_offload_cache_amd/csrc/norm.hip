@@ -170,10 +170,21 @@ __global__ __launch_bounds__((NW < 4 ? 4 : NW) * 64) void rows_kernel(RowArgs a)
 
 template <typename E, typename WE, bool NORM, bool VEC, int NW, int C>
 moe_status launch_rows(const RowArgs& a, hipStream_t st, const char* name) {
-    constexpr int ROWS = NW < 4 ? 4 / NW : 1;
-    ProfScope p(name, st);
-    rows_kernel<E, WE, NORM, VEC, NW, C><<<(unsigned)((a.T + ROWS - 1) / ROWS), (NW < 4 ? 4 : NW) * 64, 0, st>>>(a);
-    return check_launch(name);
+    constexpr int ROWS = NW < 4 ? 4 / NW : 1, THREADS = (NW < 4 ? 4 : NW) * 64;
+    constexpr int MOST = (1 << 30) / THREADS * ROWS;  // rows a launch: the grid's threads must stay below 2^32
+    RowArgs r = a;
+    for (int64_t t = 0; t < a.T; t += MOST) {
+        r.T = (int)(a.T - t < MOST ? a.T - t : MOST);
+        r.x = (const E*)a.x + t * a.ldx;
+        if (a.residual) r.residual = (const E*)a.residual + t * a.ldr, r.resid_out = (E*)a.resid_out + t * a.ldro;
+        if (a.y) r.y = (E*)a.y + t * a.ldy;
+        if (a.q) r.q = a.q + t * a.ldq, r.scale = a.scale + t * fp8_groups(a.d);
+        ProfScope p(name, st);
+        rows_kernel<E, WE, NORM, VEC, NW, C><<<(unsigned)((r.T + ROWS - 1) / ROWS), THREADS, 0, st>>>(r);
+        const moe_status s = check_launch(name);
+        if (s != MOE_OK) return s;
+    }
+    return MOE_OK;
 }
 
 template <typename E, typename WE, bool NORM, bool VEC>

@@ -83,6 +83,19 @@ def test_fp8_slot_layout(moe):
         moe.pack_expert("fp8", d, f, ew.wg, ew.wu, ew.wd)
 
 
+@pytest.mark.parametrize("d,f,k,shared", [(128, 128, 1, False), (512, 2048, 8, True), (4096, 256, 2, False)])
+def test_workspace_of_more_tokens_serves_fewer(moe, d, f, k, shared):
+    sizes = [moe.workspace_bytes(T, d, f, 64, k, shared, moe._lib.MOE_BF16, moe._lib.MOE_FP8_B128) for T in range(1, 80)]
+    assert sizes == sorted(sizes) and len(set(sizes)) > 20
+
+
+def test_product_of_too_many_rows_is_refused(moe):
+    L, p = moe.lib(), ctypes.c_void_p(256)
+    for M in (2 ** 31 - 1, 2 ** 31 - 64, 65536 * 128):
+        assert L.moe_gemm_fp8(p, 16, p, M, 16, p, 16, p, 64, p, 64, 1, None) == moe._lib.MOE_ESHAPE
+        assert b"rows exceed" in L.moe_last_error()
+
+
 def test_norm_and_quant_refusals(moe):
     L, e = moe.lib(), moe._lib
     p = ctypes.c_void_p(256)

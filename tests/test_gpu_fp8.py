@@ -216,7 +216,10 @@ def _check_product(ops, c, fast):
 
 SHAPES = [(1, 1, 16), (1, 128, 128), (1, 2048, 4096), (2, 100, 48), (3, 17, 2000), (16, 130, 256), (17, 64, 144),
           (31, 257, 1040), (33, 16, 128), (64, 512, 768), (65, 96, 384), (100, 1001, 272), (128, 640, 1024),
-          (129, 48, 16), (200, 515, 2064), (300, 1024, 512), (513, 770, 1296)]
+          (129, 48, 16), (200, 515, 2064), (300, 1024, 512), (513, 770, 1296),
+          # streaming blocks of 16 x 16, 32 x 16 and 32 x 32; the largest tiles; inputs beyond a tile's LDS
+          (16, 4096, 128), (16, 4112, 144), (16, 8200, 128), (40, 4100, 272), (2048, 8200, 272), (1050, 8192, 128),
+          (40, 64, 60000), (700, 33, 60000)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -246,6 +249,69 @@ def test_product_strides(moe, M):
         rest = torch.ones_like(big, dtype=torch.bool)
         rest[:M, 3:3 + N] = False
         assert (big[rest] == -7.0).all()
+
+
+def test_product_of_far_apart_rows(moe):
+    """Rows of the matrix further apart than a tile's 32-bit offsets reach."""
+    import torch
+
+    M, N, K, ld = 300, 5, 64, (1 << 22) + 16
+    ops, (a, sa, w, sw) = _operands(np.random.default_rng(0), M, N, K)
+    far = torch.zeros(N * ld, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).view(N, ld)
+    far[:, :K] = w
+    _check_product(ops, moe.gemm_fp8(a, sa, far[:, :K], sw), fast=False)
+
+
+def test_offsets_beyond_32_bits(moe):
+    """Rows, results and intermediate rows of more than 2^32 bytes: the last rows are right."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    rng = np.random.default_rng(0)
+    M, N, K = 2_200_000, 1024, 16
+    ops, (a, sa, w, sw) = _operands(rng, 4096, N, K)
+    a = a.view(torch.uint8).repeat(-(-M // 4096), 1)[:M].view(torch.float8_e4m3fn)
+    sa = sa.repeat(-(-M // 4096), 1)[:M].contiguous()
+    c = moe.gemm_fp8(a, sa, w, sw)
+    at = np.arange(M - 300, M) % 4096
+    _check_product((ops[0][at], ops[1][at], ops[2], ops[3]), c[M - 300:], fast=True)
+    del c, a, sa
+    T, d = 300_000, 8192
+    x = _rows(rng, 1000, d, torch.bfloat16).repeat(T // 1000, 1)
+    g = _rows(rng, 1, d, torch.bfloat16)[0].clone()
+    y, h, q, s = moe.add_rmsnorm(x, g, residual=x, emit="both")
+    _check_norm(x[-9:], x[-9:], g, 1e-6, y[-9:], h[-9:], q[-9:], s[-9:])
+    del y, h, q, s
+    q, s = moe.quant_fp8(x)
+    _check_quant(x[-9:], q[-9:], s[-9:])
+    del x, q, s
+    wl = small_workload("bf16", "fp8", 128, 2176, 2, 2)
+    li = synth.layer_inputs(wl, 64, seed=1)
+    layer = DeviceLayer.from_inputs(li)
+    T = 1 << 20
+    x = layer.x_to_device(li.x).repeat(T // 64, 1)
+    idx, tw, _, counts, offsets, perm, inv = moe.route_permute(x, layer.w_router, layer.bias, wl.k)
+    yp, _ = moe.expert_ffn_grouped(x, perm, offsets, counts, layer.slot_of_expert, layer.pool, layer.n_slots, layer.stride,
+                                   "fp8", wl.f, wl.k, y_dtype=torch.bfloat16)
+    first, last = (moe.combine(yp, tw[at].contiguous(), inv.view(T, wl.k)[at].contiguous().view(-1), wl.k, False,
+                               torch.bfloat16) for at in (slice(0, 64), slice(T - 64, T)))
+    ref = moe_layer(li.x, li.w_router, li.bias, "bf16", wl.k, wl.E, li.experts, li.shared)
+    err = rel_err_per_token(y_to_f64(last), ref["y"])
+    assert err.max() <= 0.125 and err.mean() <= 5e-3, (err.max(), err.mean())
+    assert torch.equal(first, last)
+
+
+def test_more_rows_than_one_launch_takes(moe):
+    """Narrow rows in such numbers that the threads of one grid would pass 2^32."""
+    import torch
+
+    T = (1 << 26) + 5
+    x = torch.arange(T, device="cuda", dtype=torch.float32).remainder_(997).sub_(498).view(T, 1)
+    q, s = moe.quant_fp8(x)
+    for rows in (slice(0, 1000), slice((1 << 24) - 500, (1 << 24) + 500), slice(T - 1000, T)):
+        _check_quant(x[rows], q[rows], s[rows])
+    z = x == 0  # every other value is its group's largest: +- 448
+    assert int((q.view(torch.uint8) & 127 == 0x7E).sum()) == T - int(z.sum())
 
 
 @pytest.mark.parametrize("M", [1, 20, 300])
@@ -285,7 +351,14 @@ def test_product_repeats_bitwise_on_another_stream(moe):
 CASES = [(dict(d=256, f=128, E=8, k=2, shared=True), 1), (dict(d=256, f=128, E=8, k=2, shared=True), 40),
          (dict(d=384, f=640, E=5, k=5), 3), (dict(d=128, f=128, E=1, k=1), 70), (dict(d=512, f=384, E=300, k=7), 33),
          (dict(d=640, f=256, E=16, k=4, shared=True), 64), (dict(d=256, f=256, E=6, k=2, shared=True), 65),
-         (dict(d=512, f=384, E=12, k=3), 333), (dict(d=768, f=128, E=4, k=2, shared=True), 700)]
+         (dict(d=512, f=384, E=12, k=3), 333), (dict(d=768, f=128, E=4, k=2, shared=True), 700),
+         # up to 16 tokens: waves with 2, 4 and 8 steps, equal numbers or not; the widest rows
+         (dict(d=1152, f=2176, E=3, k=2), 5), (dict(d=4224, f=1536, E=3, k=2), 16), (dict(d=4096, f=640, E=3, k=2), 16),
+         (dict(d=16384, f=128, E=2, k=1), 7), (dict(d=128, f=16384, E=2, k=1), 16),
+         # tiles: the fewest tokens, more experts than lanes cover, rows beyond the larger tiles' LDS, the largest tiles
+         (dict(d=256, f=256, E=260, k=2, shared=True), 17), (dict(d=128, f=128, E=300, k=3), 333),
+         (dict(d=12288, f=128, E=2, k=1), 130), (dict(d=128, f=16384, E=2, k=1, shared=True), 70),
+         (dict(d=2048, f=1024, E=4, k=2), 2200)]
 
 
 @pytest.mark.parametrize("shape,T", CASES, ids=[f"{c[0]['d']}x{c[0]['f']}x{c[0]['E']}_T{c[1]}" for c in CASES])
@@ -315,6 +388,59 @@ def test_layer_with_fp8_experts(moe, shape, T):
     y16 = torch.empty_like(b)
     moe.expert_ffn_grouped_noalloc(x, *args, "fp8", wl.f, wl.k, y16, shared_w=layer.shared)
     assert np.array_equal(_bits(y16), _bits(b))
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_expert_chosen_twice_and_shared_slots(moe, T):
+    """A token that chose one expert twice gets its row twice; experts that share a slot give the same rows."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    wl = small_workload("bf16", "fp8", 256, 256, 4, 3)
+    li = synth.layer_inputs(wl, T, seed=5)
+    layer = DeviceLayer.from_inputs(li)
+    soe = layer.slot_of_expert.clone()
+    soe[3] = soe[1]
+    forced = to_dev(np.tile(np.array([[1, 3, 1]], np.int32), (T, 1)), "i32")
+    out = layer.forward(layer.x_to_device(li.x), forced_idx=forced, slot_of_expert=soe)
+    rows = out["y_perm"][out["inv_perm"].long()].view(T, 3, -1)
+    assert torch.equal(rows[:, 0], rows[:, 1]) and torch.equal(rows[:, 0], rows[:, 2])
+    alone = layer.forward(layer.x_to_device(li.x), forced_idx=to_dev(np.tile(np.array([[1, 0, 2]], np.int32), (T, 1)), "i32"))
+    # the same expert in another call of T tokens: the tile differs with the counts, the order of the sums does not
+    assert torch.equal(alone["y_perm"][alone["inv_perm"].long()].view(T, 3, -1)[:, 0], rows[:, 0])
+
+
+def test_graphs_that_share_a_workspace(moe):
+    """Two captured calls of different lengths take turns on the workspace of the longer one."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    wl = small_workload("bf16", "fp8", 256, 256, 8, 4, shared=True)
+    layer = DeviceLayer.from_inputs(synth.layer_inputs(wl, 1, seed=5))
+    ws = layer.workspace(20)
+    runs = []
+    for T in (16, 20):
+        x = layer.x_to_device(synth.layer_inputs(wl, T, seed=T).x)
+        bufs = dict(layer.buffers(T), ws=ws)
+        want = layer.forward(x)["y"].clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            layer.forward(x, bufs=bufs)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.forward(x, bufs=bufs)
+        runs.append((g, bufs["y"], want, x, bufs))  # a graph keeps no tensor alive
+    for _ in range(3):
+        for g, y, want, *_ in runs:
+            y.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+    del g, runs
+    gc.collect()
 
 
 @pytest.mark.parametrize("T", [2, 90, 400])
