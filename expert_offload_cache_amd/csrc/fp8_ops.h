@@ -22,6 +22,8 @@ struct GemmFp8 {
     int c_vec;   // rows of c start on 16 bytes
 };
 
+inline int64_t blocks_of(int64_t n, int block) { return (n + block - 1) / block; }
+
 // four consecutive columns n .. of row m of c
 __device__ __forceinline__ void store_c4(const GemmFp8& g, int m, int n, f32x4_t v) {
     if (g.c_vec && n + 3 < g.N) {

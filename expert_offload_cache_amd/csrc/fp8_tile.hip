@@ -334,7 +334,6 @@ __device__ __forceinline__ void store_rows(const f32x4_t (&acc)[RA][NTB], uint8_
 // ---- the dense product ------------------------------------------------------------------------------
 template <int RA, int NTB, int NW, int RW, int RX, bool EXACT, bool TAIL>
 __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
-    constexpr int W = true;
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     typedef std::conditional_t<EXACT, float, uint16_t> OutT;  // binary32 results are the exact ones
     extern __shared__ __align__(16) uint8_t smem[];
@@ -372,7 +371,7 @@ moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
     auto kern = tail ? gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, EXACT, true> : gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, EXACT, false>;
     const int lds = TL::lds(g.G);
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
-    const dim3 grid((unsigned)((g.N + TL::kMT - 1) / TL::kMT), (unsigned)((g.M + TL::kNT - 1) / TL::kNT));
+    const dim3 grid((unsigned)blocks_of(g.N, TL::kMT), (unsigned)blocks_of(g.M, TL::kNT));
     ProfScope p("gemm_fp8_tile", st);
     kern<<<grid, NW * 64, lds, st>>>(g);
     return check_launch("gemm_fp8_tile");
@@ -590,7 +589,7 @@ const void* gemm_fp8_best_tile(const GemmFp8& g, float& us) {
     us = 0.f;
     if (g.ldw > (1u << 22)) return nullptr;  // a tile's weight offsets have 32 bits
     auto look = [&](const TileCost& t) {
-        const int64_t rows = (g.M + t.nt - 1) / t.nt, tiles = (int64_t)((g.N + t.mt - 1) / t.mt) * rows;
+        const int64_t rows = blocks_of(g.M, t.nt), tiles = blocks_of(g.N, t.mt) * rows;
         if (t.lds(g.G) > kLds || rows > 65535) return;
         const float rounds = (float)((tiles + kCUs - 1) / kCUs);
         const float e = 3.0f + g.G * std::max(t.alone, rounds * t.full);
