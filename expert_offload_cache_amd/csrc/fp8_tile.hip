@@ -30,6 +30,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(1))) void* gbl_ptr_t;
 
 constexpr int kLds = 160 << 10;  // LDS of a compute unit
+constexpr int kXCDs = 8;         // workgroup i runs on XCD i mod 8
 constexpr int kCUs = 256;        // compute units (a multiple of the 8 XCDs)
 
 enum { kDense = 2 };  // beside kGateUp and kDown
@@ -378,6 +379,8 @@ moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
 }
 
 // ---- the routed experts' projections ------------------------------------------------------------------
+__device__ __forceinline__ int64_t ceil_of(int64_t n, int block) { return (n + block - 1) / block; }
+
 // The chunks of nt tokens of the experts that hold n_lo to n_hi (every lane gets the sum).
 __device__ __forceinline__ int count_chunks(const FfnArgs& a, int nt, int n_lo, int n_hi) {
     auto chunks = [&](int n) { return n >= n_lo && n <= n_hi ? (n + nt - 1) / nt : 0; };
@@ -388,15 +391,21 @@ __device__ __forceinline__ int count_chunks(const FfnArgs& a, int nt, int n_lo, 
     return __builtin_amdgcn_readfirstlane(c) + (a.shared_w ? chunks(a.T) : 0);
 }
 
-// This workgroup's tiles (first, first + gridDim.x, ...) of the experts that hold n_lo to n_hi tokens.
+// This workgroup's tiles of the experts that hold n_lo to n_hi tokens (chunks: their chunks of kNT).  Workgroup
+// i runs on XCD i mod 8; each XCD takes a run of consecutive tiles, so that the tiles that read the same
+// weights or the same tokens share an L2 (2048 tokens, 8 of 128 experts of 2048 x 768: 254 -> 236 us against tiles
+// dealt out in turn, 8192 on 7 of 4096 x 2048: 1597 -> 1526).
 template <int MODE, int RA, int NTB, int NW, int RW, int RX>
-__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_lo, int n_hi, int64_t first) {
+__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     static_assert(MODE != kGateUp || (RA % 2 == 0 && TL::kMT % 256 == 0), "gate/up tiles hold whole groups of h");
     const FfnArgs& a = p.a;
     const int nblk = MODE == kGateUp ? 2 * (a.f / 16) : a.d / 16;
     const int gx = (nblk + NW * RA - 1) / (NW * RA);  // tiles over the weight rows
-    for (int64_t id = first;; id += gridDim.x) {
+    const int64_t n = (int64_t)chunks * gx, per = ceil_of(n, kXCDs);
+    for (int64_t at = first / kXCDs; at < per; at += gridDim.x / kXCDs) {
+        const int64_t id = (first % kXCDs) * per + at;
+        if (id >= n) return;
         // The empty asm statements make these values new in each pass: otherwise everything that depends on
         // them alone is computed before the loop and held in registers across it, which spills.
         int tid = threadIdx.x, K = MODE == kGateUp ? a.d : a.f;
@@ -516,10 +525,16 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_
     }
 }
 
-// Experts with up to kLight tokens take 256-row x 64-token tiles, with the weights two steps ahead: their
-// weights' bytes bound them.  The others take 512 x 128, or 256 x 128 where that still leaves every
-// tile a compute unit of its own (517 tokens on 8 of 128 experts: LIGHT_GAIN).  HEAVY false: no expert of
-// the call can hold more, or the larger tiles' scales exceed the LDS (inputs beyond 11776).
+// The tiles of a call (measured, us of the gate/up projection, 512 x 128 / 256 x 128 / 256 x 64 tiles, experts of
+// 2048 x 768 or, from 7 experts on, 4096 x 2048):
+// - All experts 256 rows x 64 tokens where each such tile has a compute unit of its own: 128 tokens on each of 8
+//   experts 44 / 29 / 21, 70 on each of 7 72 / 48 / 39.
+// - Else experts with up to kLight tokens take 256 x 64, with the weights two steps ahead (their weights' bytes
+//   bound them), and the others 512 x 128 or 256 x 128, whichever needs the less time for its rounds over the
+//   compute units at 2.1 and 1.27 us a step (the dense product's costs): 384 tokens on each of 8 44 / 28 / 35,
+//   1000 on each of 8 50 / 55 / 53, 517 on each of 7 136 / 127 / 123, 4096 on each of 7 522 / 608 / 765.
+// HEAVY false: no expert of the call can hold more than kLight, or the larger tiles' scales exceed the LDS
+// (inputs beyond 11776).
 constexpr int kLight = 64, kMost = 1 << 30, kWaves = 8;
 typedef Tile8<4, 8, kWaves, 1, 3> TileLarge;
 typedef Tile8<2, 8, kWaves, 2, 3> TileMid;
@@ -530,20 +545,23 @@ typedef Tile8<2, 4, kWaves, 2, 4> TileLight;
 template <int MODE, bool HEAVY>
 __global__ __launch_bounds__(kWaves * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    int64_t first = blockIdx.x;
-    if constexpr (HEAVY) {
-        const int64_t rows = MODE == kGateUp ? 2 * p.a.f : p.a.d, chunks = count_chunks(p.a, TileLarge::kNT, kLight + 1, kMost);
-        int64_t tiles = chunks * ((rows + TileLarge::kMT - 1) / TileLarge::kMT);
-        if (tiles > kCUs / 2) {
-            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, smem, kLight + 1, kMost, first);
+    const int rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
+    int first = blockIdx.x, light = kMost;  // the 256 x 64 tiles take experts with up to `light` tokens
+    if (HEAVY && (int64_t)count_chunks(p.a, TileLight::kNT, 0, kMost) * ceil_of(rows, TileLight::kMT) > kCUs) {
+        light = kLight;
+        const int chunks = count_chunks(p.a, TileLarge::kNT, kLight + 1, kMost);
+        int64_t tiles = (int64_t)chunks * ceil_of(rows, TileLarge::kMT);
+        const int64_t mid = (int64_t)chunks * ceil_of(rows, TileMid::kMT);
+        if ((float)ceil_of(tiles, kCUs) * 2.1f < (float)ceil_of(mid, kCUs) * 1.27f) {
+            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, smem, kLight + 1, kMost, chunks, first);
         } else {
-            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, smem, kLight + 1, kMost, first);
-            tiles = chunks * ((rows + TileMid::kMT - 1) / TileMid::kMT);
+            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, smem, kLight + 1, kMost, chunks, first);
+            tiles = mid;
         }
-        // the light tiles begin with the workgroup that the heavy ones' last round did not reach
-        first = (blockIdx.x + gridDim.x - tiles % gridDim.x) % gridDim.x;
+        // the light tiles begin with the workgroup, of the same XCD, that the heavy ones' last round did not reach
+        first = (int)((blockIdx.x + gridDim.x - (int64_t)ceil_of(tiles, kXCDs) * kXCDs % gridDim.x) % gridDim.x);
     }
-    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, smem, 0, HEAVY ? kLight : kMost, first);
+    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, smem, 0, light, count_chunks(p.a, TileLight::kNT, 0, light), first);
 }
 
 template <int MODE, bool HEAVY>
@@ -554,7 +572,7 @@ moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     const int64_t tiles = work_items(p.a, TileLight::kNT) * ((rows + TileLight::kMT - 1) / TileLight::kMT);
     ProfScope sc(name, st);
-    kern<<<(unsigned)std::min<int64_t>(tiles, kCUs), kWaves * 64, lds, st>>>(p);
+    kern<<<(unsigned)std::min<int64_t>(blocks_of(tiles, kXCDs) * kXCDs, kCUs), kWaves * 64, lds, st>>>(p);
     return check_launch(name);
 }
 
