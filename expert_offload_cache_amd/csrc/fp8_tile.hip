@@ -105,7 +105,8 @@ struct Feed {
     const uint8_t* x[UN];
 };
 
-// acc = the tile's products over all steps.  MODE decides which scale a row block takes.
+// acc = the tile's products over its nst steps, of which the first `given` exist (TAIL: the rest are
+// scaled by 0 and load nothing of the rows).  MODE decides which scale a row block takes.
 //
 // The products are software-pipelined by hand across the steps' ends: a product is folded into its
 // accumulator four products later, so the vector unit's four multiply-adds run while the matrix core
@@ -117,7 +118,7 @@ struct Feed {
 // its last product is on its way; in the next step's first block the slot they left is filled again.
 template <int MODE, int RA, int NTB, int NW, int RW, int RX, int W, bool EXACT, bool TAIL, typename SX, typename SW>
 __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW, RX>::kUnits, W>& fd, uint8_t* smem, int nst,
-                                          int K, int wv, int lane, int tid, SX&& x_scales, SW&& w_scales,
+                                          int given, int K, int wv, int lane, int tid, SX&& x_scales, SW&& w_scales,
                                           f32x4_t (&acc)[RA][NTB]) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     constexpr int UN = TL::kUnits, WN = 2 * RA;  // token and weight loads of a step
@@ -252,12 +253,12 @@ __device__ __forceinline__ void tile_loop(const Feed<RA, Tile8<RA, NTB, NW, RW, 
 #pragma unroll 4
         for (int i = tid; i < nst * TL::kNT; i += NW * 64) {
             const int t = i / nst, k = i - t * nst;
-            to[k * (TL::kNT + 1) + t] = x_scales(t)[k];
+            to[k * (TL::kNT + 1) + t] = !TAIL || k < given ? x_scales(t)[k] : 0.f;
         }
         to += (size_t)nst * (TL::kNT + 1);
         for (int i = tid; i < nst * TL::kWScales; i += NW * 64) {
             const int b = i / nst, k = i - b * nst;
-            to[k * TL::kWScales + b] = w_scales(b)[k];
+            to[k * TL::kWScales + b] = !TAIL || k < given ? w_scales(b)[k] : 0.f;
         }
     }
     // weights and tokens of step 0 have landed
@@ -333,30 +334,62 @@ __device__ __forceinline__ void store_rows(const f32x4_t (&acc)[RA][NTB], uint8_
 }
 
 // ---- the dense product ------------------------------------------------------------------------------
-template <int RA, int NTB, int NW, int RW, int RX, bool EXACT, bool TAIL>
-__global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
+// KG groups of NW waves each take a run of steps of the same tile, in an LDS area of their own, and join their sums
+// in group order: where there are fewer tiles than compute units, half the steps one after the other.
+template <int RA, int NTB, int NW, int RW, int RX, int KG>
+struct GemmTile : Tile8<RA, NTB, NW, RW, RX> {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
+    static constexpr int group_lds(int G) { return (TL::lds((G + KG - 1) / KG) + 15) / 16 * 16; }
+    static constexpr int gemm_lds(int G) { return KG * group_lds(G); }
+};
+
+template <int RA, int NTB, int NW, int RW, int RX, int KG, bool EXACT, bool TAIL>
+__global__ __launch_bounds__(NW * KG * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
+    using TL = GemmTile<RA, NTB, NW, RW, RX, KG>;
     typedef std::conditional_t<EXACT, float, uint16_t> OutT;  // binary32 results are the exact ones
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 63;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = KG > 1 ? wave / NW : 0, wv = wave - kg * NW;
     const int n0 = blockIdx.x * TL::kMT, m0 = blockIdx.y * TL::kNT;
     const int nrow = n0 + wv * RA * 16;  // this wave's first weight row
+    const int nst = (g.G + KG - 1) / KG, s0 = kg * nst;  // this group's steps
+    uint8_t* mine = smem + kg * TL::group_lds(g.G);
     Feed<RA, TL::kUnits, kWRows> fd;
-    fd.w = g.w + (size_t)n0 * g.ldw;
+    fd.w = g.w + (size_t)n0 * g.ldw + (size_t)s0 * kFp8Group;
 #pragma unroll
     for (int u = 0; u < 2 * RA; ++u)  // rows past the end repeat the last one and are not stored
         fd.w_off[u] = (uint32_t)(min(nrow + 8 * u + (lane >> 3), g.N - 1) - n0) * (uint32_t)g.ldw + 16 * chunk_of_lane(lane);
 #pragma unroll
     for (int u = 0; u < TL::kUnits; ++u) {
         const int m = min(m0 + 8 * (wv * TL::kUnits + u) + (lane >> 3), g.M - 1);
-        fd.x[u] = g.a + (size_t)m * g.lda + 16 * chunk_of_lane(lane);
+        fd.x[u] = g.a + (size_t)m * g.lda + (size_t)s0 * kFp8Group + 16 * chunk_of_lane(lane);
     }
     f32x4_t acc[RA][NTB];
     tile_loop<kDense, RA, NTB, NW, RW, RX, kWRows, EXACT, TAIL>(
-        fd, smem, g.G, g.K, wv, lane, threadIdx.x, [&](int t) { return g.a_scale + (size_t)min(m0 + t, g.M - 1) * g.G; },
-        [&](int b) { return g.w_scale + (size_t)(min(n0 + 128 * b, g.N - 1) / 128) * g.G; }, acc);
-    // the ring is free: every wave has left it
+        fd, mine, nst, min(nst, g.G - s0), g.K - s0 * kFp8Group, wv, lane, KG > 1 ? wv * 64 + lane : threadIdx.x,
+        [&](int t) { return g.a_scale + (size_t)min(m0 + t, g.M - 1) * g.G + s0; },
+        [&](int b) { return g.w_scale + (size_t)(min(n0 + 128 * b, g.N - 1) / 128) * g.G + s0; }, acc);
+    // the rings are free: every wave has left them
+    if constexpr (KG > 1) {
+        static_assert(KG == 2 && NW * RA * NTB * 1024 <= RX * TL::kStage + RW * TL::kWBytes, "the second group's sums");
+        float4* sums = (float4*)(smem + TL::group_lds(g.G)) + (size_t)wv * RA * NTB * 64 + lane;
+        if (kg == 1) {
+#pragma unroll
+            for (int i = 0; i < RA; ++i)
+#pragma unroll
+                for (int j = 0; j < NTB; ++j)
+                    sums[(i * NTB + j) * 64] = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        }
+        __syncthreads();
+        if (kg == 1) return;
+#pragma unroll
+        for (int i = 0; i < RA; ++i)
+#pragma unroll
+            for (int j = 0; j < NTB; ++j) {
+                const float4 t = sums[(i * NTB + j) * 64];
+                acc[i][j][0] += t.x, acc[i][j][1] += t.y, acc[i][j][2] += t.z, acc[i][j][3] += t.w;
+            }
+    }
     static_assert(NW * 8192 <= RX * TL::kStage + RW * TL::kWBytes, "the waves' 8 KB");
     uint8_t* area = smem + wv * 8192;
     auto row = [&](int t) __attribute__((always_inline)) {
@@ -365,16 +398,17 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_fp8_tile_kernel(GemmFp8 g) {
     store_rows<OutT>(acc, area, lane, g.N - nrow, g.c_vec, row);
 }
 
-template <int RA, int NTB, int NW, int RW, int RX, bool EXACT>
+template <int RA, int NTB, int NW, int RW, int RX, int KG, bool EXACT>
 moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
-    using TL = Tile8<RA, NTB, NW, RW, RX>;
-    const bool tail = g.K % 128 != 0;
-    auto kern = tail ? gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, EXACT, true> : gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, EXACT, false>;
-    const int lds = TL::lds(g.G);
+    using TL = GemmTile<RA, NTB, NW, RW, RX, KG>;
+    const bool tail = g.K % 128 != 0 || g.G % KG != 0;
+    auto kern = tail ? gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, KG, EXACT, true>
+                     : gemm_fp8_tile_kernel<RA, NTB, NW, RW, RX, KG, EXACT, false>;
+    const int lds = TL::gemm_lds(g.G);
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     const dim3 grid((unsigned)blocks_of(g.N, TL::kMT), (unsigned)blocks_of(g.M, TL::kNT));
     ProfScope p("gemm_fp8_tile", st);
-    kern<<<grid, NW * 64, lds, st>>>(g);
+    kern<<<grid, NW * KG * 64, lds, st>>>(g);
     return check_launch("gemm_fp8_tile");
 }
 
@@ -455,7 +489,7 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_
             fd.x[u] = x + (size_t)source(8 * (wv * TL::kUnits + u) + (lane >> 3)) * K + 16 * chunk_of_lane(lane);
         f32x4_t acc[RA][NTB];
         tile_loop<MODE, RA, NTB, NW, RW, RX, kWFrags, false, false>(
-            fd, smem, G, K, wv, lane, tid, [&](int t) { return x_scale + (size_t)source(t) * G; },
+            fd, smem, G, G, K, wv, lane, tid, [&](int t) { return x_scale + (size_t)source(t) * G; },
             [&](int s) {
                 // gate/up: the gate and the up scale of each 128 columns of h (16 blocks); down: of 8 blocks
                 const int b = min(bw + (MODE == kGateUp ? 16 * (s >> 1) + (s & 1) : 8 * s),
@@ -579,27 +613,33 @@ moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
 }  // namespace
 
 // The tiles, and what a 128-input step of one costs (us): alone on a compute unit, and where every unit
-// has a full share of them.  Measured on 32-step products of 256 to 8192 rows; a product's time follows as
-// 3 us + steps * max(alone, rounds * full) to within 15 % over 64 .. 8192 rows and 512 .. 8192 columns.
-// Large tiles read less from LDS a product, small ones fill the chip with fewer rows.
+// has a full share of them.  A product's time follows as 3 us + steps * max(alone, rounds * full), to within 15 %
+// over 64 to 8192 rows and 512 to 8192 columns of row-major matrices whose rows are whole cache lines.
+// Large tiles read less from LDS a product, small ones fill the chip with fewer rows, and two groups that share
+// a tile's steps fill it with fewer still.  Measured, us, rows x N x K, one tile against the next:
+// 512 x 2048 x 4096 64x64 in two groups 12.7, in one 16.0; 1000 x 2048 x 4096 128x64 in two groups 17.2, in one
+// 19.6, 64x64 in two groups 19.1 (one step ahead: two workgroups a unit) or 23.0; 1000 x 4096 x 2048 256x64 15.8,
+// 128x64 17.1; 2048 x 4096 x 2048 256x128 25.3, 256x64 28.2; 8192 x 4096 x 4096 512x128 131, 256x128 164.
 namespace {
 struct TileCost {
-    int mt, nt;
+    int mt, nt, groups;
     float alone, full;
     int (*lds)(int G);
     moe_status (*launch)(const GemmFp8&, hipStream_t);
 };
-template <int RA, int NTB, int NW, int RW, int RX, bool EXACT>
+template <int RA, int NTB, int NW, int RW, int RX, int KG, bool EXACT>
 constexpr TileCost cost(float alone, float full) {
-    using TL = Tile8<RA, NTB, NW, RW, RX>;
-    return {TL::kMT, TL::kNT, alone, full, TL::lds, launch_gemm<RA, NTB, NW, RW, RX, EXACT>};
+    using TL = GemmTile<RA, NTB, NW, RW, RX, KG>;
+    return {TL::kMT, TL::kNT, KG, alone, full, TL::gemm_lds, launch_gemm<RA, NTB, NW, RW, RX, KG, EXACT>};
 }
 constexpr TileCost kTiles[] = {
-    cost<4, 8, 8, 1, 3, false>(1.70f, 2.10f), cost<2, 8, 8, 2, 3, false>(0.99f, 1.27f),
-    cost<2, 4, 8, 2, 4, false>(0.66f, 0.74f), cost<2, 4, 4, 2, 4, false>(0.49f, 0.36f),
-    cost<1, 4, 4, 2, 4, false>(0.39f, 0.255f)};
-constexpr TileCost kExactTiles[] = {cost<2, 8, 8, 1, 4, true>(1.70f, 2.04f), cost<2, 4, 4, 3, 5, true>(0.75f, 0.78f),
-                                    cost<1, 4, 4, 3, 5, true>(0.60f, 0.45f)};
+    cost<4, 8, 8, 1, 3, 1, false>(1.70f, 2.10f), cost<2, 8, 8, 2, 3, 1, false>(0.95f, 1.27f),
+    cost<2, 4, 8, 2, 4, 1, false>(0.66f, 0.77f), cost<2, 4, 4, 2, 4, 1, false>(0.49f, 0.40f),
+    cost<1, 4, 4, 2, 4, 1, false>(0.39f, 0.27f), cost<2, 4, 4, 2, 4, 2, false>(0.82f, 0.90f),
+    cost<1, 4, 4, 2, 4, 2, false>(0.57f, 0.65f), cost<1, 4, 4, 1, 3, 2, false>(0.68f, 0.50f)};
+constexpr TileCost kExactTiles[] = {
+    cost<2, 8, 8, 1, 4, 1, true>(1.70f, 2.10f), cost<2, 4, 4, 3, 5, 1, true>(0.72f, 0.78f),
+    cost<1, 4, 4, 3, 5, 1, true>(0.61f, 0.45f), cost<1, 4, 4, 2, 4, 2, true>(0.88f, 0.95f)};
 }  // namespace
 
 const void* gemm_fp8_best_tile(const GemmFp8& g, float& us) {
@@ -610,7 +650,7 @@ const void* gemm_fp8_best_tile(const GemmFp8& g, float& us) {
         const int64_t rows = blocks_of(g.M, t.nt), tiles = blocks_of(g.N, t.mt) * rows;
         if (t.lds(g.G) > kLds || rows > 65535) return;
         const float rounds = (float)((tiles + kCUs - 1) / kCUs);
-        const float e = 3.0f + g.G * std::max(t.alone, rounds * t.full);
+        const float e = 3.0f + (float)blocks_of(g.G, t.groups) * std::max(t.alone, rounds * t.full);
         if (!best || e < us) best = &t, us = e;
     };
     if (g.c_bf16)

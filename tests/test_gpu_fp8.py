@@ -219,7 +219,11 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (1, 2048, 4096), (2, 100, 48), (3, 17, 2000
           (129, 48, 16), (200, 515, 2064), (300, 1024, 512), (513, 770, 1296),
           # streaming blocks of 16 x 16, 32 x 16 and 32 x 32; the largest tiles; inputs beyond a tile's LDS
           (16, 4096, 128), (16, 4112, 144), (16, 8200, 128), (40, 4100, 272), (2048, 8200, 272), (1050, 8192, 128),
-          (40, 64, 60000), (700, 33, 60000)]
+          (40, 64, 60000), (700, 33, 60000),
+          # a tile's steps in two groups: an odd number of them, one, rows that end inside one
+          (200, 512, 640), (400, 2048, 2064), (1000, 1024, 1040), (1000, 1001, 2000), (20000, 128, 1152), (20000, 64, 1600),
+          # the larger tiles, whole and ragged
+          (2048, 8192, 400), (2048, 2048, 1040), (2040, 4090, 528), (1000, 2000, 1552)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
