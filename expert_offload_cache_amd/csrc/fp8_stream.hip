@@ -13,6 +13,11 @@
 // activations are small and come from the caches).  Activations that are not yet in 8 bits
 // (bf16 x of a layer, the binary32 h between the projections) are quantised as they are loaded: the
 // four lanes l, l ^ 16, l ^ 32, l ^ 48 hold the 128 inputs of a token's group between them.
+//
+// Experts: one token on 6 of 256 experts of 4096 x 2048 and the shared one (176 MB) 25 + 13.5 us, 4.6 TB/s; 16 tokens
+// on 56 of them 233 us, 5.5 TB/s (with the tokens prepared again for each row block: 453).
+// Dense: one row against 4096 x 2048 (8.4 MB) 4.4 us, of which 3 are a launch and its first loads; 37 rows against
+// 2048 x 4096 9.6 us, bound by the chain of a wave's 4 steps (loads, widening, four products, four multiply-adds).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -177,7 +182,7 @@ __device__ __forceinline__ void join_waves(const f32x4_t (&acc)[NU], int w, int 
 }
 
 // ---- up to 16 tokens ----------------------------------------------------------------------------------
-// One token block, RBW row blocks a workgroup: the wave's token operands (NS steps) are prepared once and stay
+// One token block, RBW row blocks a workgroup (4: 16 KB of weights in flight a wave at a ring of 8): the wave's token operands (NS steps) are prepared once and stay
 // in registers, and its RBW * NS weight fragments stream through a ring of D.  frag(i, ks): this lane's
 // first 16 bytes of row block i at step ks, the second half kFp8Frag / 2 on; wscale(i): the block's scales.
 // EVEN: S * NS = nst, every wave has NS steps; else wave w has those of w, w + S, ... that exist.
@@ -359,7 +364,8 @@ moe_status launch_rows(const FfnFp8& p, int S, hipStream_t st, const char* name)
     return check_launch(name);
 }
 
-// S waves that split nst steps, NS each at most
+// S waves that split nst steps, NS each at most: 4 to 8 waves, which leaves two workgroups a compute unit, with as few
+// steps each as that allows
 struct Split {
     int S, NS;
     bool even;

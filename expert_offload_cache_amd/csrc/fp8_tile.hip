@@ -14,6 +14,14 @@
 // Gate/up: a wave's row blocks are gate and up blocks in turn, so SwiGLU happens in registers; the
 // 16 / RA waves that share a 128-column group of h join their largest magnitudes through LDS, and h is
 // written in 8 bits with its scale.
+//
+// Measured: 8192 x 4096 x 4096 in 131 us, 2.1 PFLOP/s; 8192 tokens on 6 of 256 experts of 4096 x 2048 and the shared
+// one, the six the same, 952 + 540 us, 1.9 PFLOP/s.  Counters of the first: the matrix cores are busy 56 % of the units'
+// cycles (2.0 GHz under this load), the vector units about as much (four multiply-adds a product and one instruction
+// more), LDS 28 %, bank conflicts 3 % of that; the loop holds 32 products in 285 instructions.  What is left is two
+// waves a SIMD that both wait at a step's barrier and for operands one block ahead: the accumulators, 128 registers,
+// leave no room for a third wave or a longer lead (reading two token blocks ahead, 32 x 32 products and buffer
+// loads to LDS gained nothing).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -189,7 +189,9 @@ MOE_API moe_status moe_route_permute(const void* x, moe_dtype act, int T, int d,
  * Intermediate h is rounded to bf16 when act is BF16 (binary32 when act is F32).
  * Weights FP8_B128 need act BF16: each row of x is quantised (see FP8 above), the gate and up sums
  * are of 8-bit products, h is quantised from its binary32 values and the down projection's products
- * are of 8-bit values again: bitwise what moe_quant_fp8 and moe_expert_ffn_fp8 give. */
+ * are of 8-bit values again: bitwise what moe_quant_fp8 and moe_expert_ffn_fp8 give.  Calls of up to
+ * 16 tokens sum in binary32; above, a 128-input group's sum is the matrix core's own (see
+ * moe_gemm_fp8), so a token's row may differ in its last bits between the two. */
 #define MOE_SLOT_ELSEWHERE (-2)
 /* Above 64 tokens (prefill) the experts run on the matrix-core grouped GEMM, which feeds int4
  * weights to the matrix cores as bf16(q * s).  Experts holding at most moe_prefill_gemv_tokens(w)
@@ -209,7 +211,7 @@ MOE_API moe_status moe_expert_ffn_grouped(const void* x, moe_dtype act, int T, i
 /* moe_expert_ffn_grouped with FP8_B128 weights for rows that are already quantised (by moe_add_rmsnorm
  * or moe_quant_fp8): x e4m3 [T,d] (rows back to back, 16-byte aligned), x_scale binary32 [T, d/128].
  * y_dtype F32 or BF16.  ws: moe_workspace_bytes(T, d, f, E, k, has_shared, MOE_BF16, MOE_FP8_B128)
- * bytes.  Everything else as moe_expert_ffn_grouped. */
+ * bytes (never less than fewer tokens take).  Everything else as moe_expert_ffn_grouped. */
 MOE_API moe_status moe_expert_ffn_fp8(const void* x, const float* x_scale, int T, int d, int f, int E, int k,
                                       const int32_t* perm, const int32_t* offsets, const int32_t* counts,
                                       const int32_t* slot_of_expert, int n_slots, const void* slot_pool,
@@ -272,11 +274,17 @@ MOE_API moe_status moe_quant_fp8(const void* x, moe_dtype act, int T, int d, siz
 /* moe_gemm_fp8 -- the product of quantised rows and a quantised matrix (a layer's projections next
  * to its experts):
  *   c[m,n] = sum_g a_scale[m,g] * w_scale[n/128,g] * sum_{k in group g} a[m,k] * w[n,k],
- * products of e4m3 values and their sums in binary32, each c rounded once to out (F32 or BF16).
+ * each c rounded once to out (F32 or BF16).  The groups' terms are added in binary32, each times
+ * a_scale * w_scale, formed first: that product has to be finite.  Within a group: out F32 sums
+ * the exact products in binary32; out BF16 may leave it to the matrix core, which drops what falls
+ * below some 2^-18 of a group's largest product (1.5e-5 of a result, against the rounding's 2^-8).
+ * Which it is, and the order of the sums, follow from M, N and K: a row may differ in its last bits
+ * between calls of different M, never between calls of the same shape.
  *   a [M,K] e4m3, a_scale [M, ceil(K/128)]; w [N,K] e4m3 (rows are outputs), w_scale
  *   [ceil(N/128), ceil(K/128)]; c [M,N].  lda, ldw, ldc: elements from a row to the next.
- * K a multiple of 16 (the last group may be shorter); rows of a and w start on 16 bytes; M and N
- * are free.  c overlaps none of the inputs. */
+ * K a multiple of 16 up to 2^20 (the last group may be shorter); rows of a and w start on 16 bytes; N
+ * up to 2^24, M up to 2 million rows at the least (MOE_ESHAPE beyond one launch).  Rows
+ * that start on whole cache lines (128 bytes) are faster.  c overlaps none of the inputs. */
 MOE_API moe_status moe_gemm_fp8(const void* a, size_t lda, const float* a_scale, int M, int K, const void* w,
                                 size_t ldw, const float* w_scale, int N, void* c, size_t ldc, moe_dtype out,
                                 moe_stream s);
