@@ -75,6 +75,12 @@ __device__ __forceinline__ f32x4_t mfma_fp8(i32x8_t a, i32x8_t b) {
 typedef __bf16 bf16v2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16v8_t __attribute__((ext_vector_type(8)));
 
+// two values rounded to bf16 (nearest even) by the hardware's conversion, the first in the low half
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16v2_t));
+}
+
 struct Wide8 {  // a lane's 32 inputs as bf16
     bf16v8_t v[4];
 };

@@ -29,8 +29,8 @@ __device__ __forceinline__ void store_c4(const GemmFp8& g, int m, int n, f32x4_t
     if (g.c_vec && n + 3 < g.N) {
         if (g.c_bf16) {
             uint2 o;
-            o.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
-            o.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
+            o.x = bf16_pair(v[0], v[1]);
+            o.y = bf16_pair(v[2], v[3]);
             *(uint2*)((uint16_t*)g.c + (size_t)m * g.ldc + n) = o;
         } else {
             *(float4*)((float*)g.c + (size_t)m * g.ldc + n) = make_float4(v[0], v[1], v[2], v[3]);
