@@ -444,11 +444,23 @@ __device__ __forceinline__ float silu_mul_quick(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.442695041f)) * u;
 }
 
+// The experts' counts and slots in LDS, for up to kTableExperts (more are read from memory): a tile's item is then
+// found without waiting for memory, where a load waits behind the stores of the tile before.
+constexpr int kTableExperts = 256, kTable = 8 * kTableExperts;  // bytes
+__device__ __forceinline__ void fill_table(const FfnArgs& a, uint8_t* table) {
+    for (int e = threadIdx.x; e < min(a.E, kTableExperts); e += blockDim.x) {
+        ((int32_t*)table)[e] = a.counts[e];
+        ((int32_t*)table)[kTableExperts + e] = a.slot_of_expert[e];
+    }
+    __syncthreads();
+}
+
 // The chunks of nt tokens of the experts that hold n_lo to n_hi (every lane gets the sum).
-__device__ __forceinline__ int count_chunks(const FfnArgs& a, int nt, int n_lo, int n_hi) {
+__device__ __forceinline__ int count_chunks(const FfnArgs& a, const uint8_t* table, int nt, int n_lo, int n_hi) {
     auto chunks = [&](int n) { return n >= n_lo && n <= n_hi ? (n + nt - 1) / nt : 0; };
     int c = 0;
-    for (int e = threadIdx.x & 63; e < a.E; e += 64) c += chunks(a.counts[e]);
+    for (int e = threadIdx.x & 63; e < a.E; e += 64)
+        c += chunks(e < kTableExperts ? ((const int32_t*)table)[e] : a.counts[e]);
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) c += __shfl_xor(c, s, 64);
     return __builtin_amdgcn_readfirstlane(c) + (a.shared_w ? chunks(a.T) : 0);
@@ -459,7 +471,7 @@ __device__ __forceinline__ int count_chunks(const FfnArgs& a, int nt, int n_lo, 
 // weights or the same tokens share an L2 (2048 tokens, 8 of 128 experts of 2048 x 768: 254 -> 236 us against tiles
 // dealt out in turn, 8192 on 7 of 4096 x 2048: 1597 -> 1526).
 template <int MODE, int RA, int NTB, int NW, int RW, int RX>
-__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
+__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const uint8_t* table, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     static_assert(MODE != kGateUp || (RA % 2 == 0 && TL::kMT % 256 == 0), "gate/up tiles hold whole groups of h");
     const FfnArgs& a = p.a;
@@ -476,7 +488,12 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_
         const int lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), G = K / 128;
         const int bx = (int)(id % gx);
         int e, chunk, slot, n_all, p0;
-        if (!find_item(a, TL::kNT, (int)(id / gx), e, chunk, slot, n_all, p0, n_lo, n_hi)) return;
+        const bool any = a.E <= kTableExperts
+                             ? find_work_slot<kTableExperts / 64>((const int32_t*)table, (const int32_t*)table + kTableExperts,
+                                                                  a.E, a.T, a.k, TL::kNT, a.shared_w != nullptr, (int)(id / gx),
+                                                                  e, chunk, slot, n_all, p0, n_lo, n_hi)
+                             : find_item(a, TL::kNT, (int)(id / gx), e, chunk, slot, n_all, p0, n_lo, n_hi);
+        if (!any) return;
         const bool shared = e == -1;
         const int nt = min(TL::kNT, n_all - chunk * TL::kNT);
         p0 += chunk * TL::kNT;  // first row of the tile
@@ -597,7 +614,7 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, uint8_t* smem, int n_
 //   compute units at 2.1 and 1.27 us a step (the dense product's costs): 384 tokens on each of 8 44 / 28 / 35,
 //   1000 on each of 8 50 / 55 / 53, 517 on each of 7 136 / 127 / 123, 4096 on each of 7 522 / 608 / 765.
 // HEAVY false: no expert of the call can hold more than kLight, or the larger tiles' scales exceed the LDS
-// (inputs beyond 11776).
+// (inputs beyond 11264).
 constexpr int kLight = 64, kMost = 1 << 30, kWaves = 8;
 typedef Tile8<4, 8, kWaves, 1, 3> TileLarge;
 typedef Tile8<2, 8, kWaves, 2, 3> TileMid;
@@ -607,30 +624,32 @@ typedef Tile8<2, 4, kWaves, 2, 4> TileLight;
 // the counts give is through (a launch for the most there could be took 19 to 58 us to find nothing).
 template <int MODE, bool HEAVY>
 __global__ __launch_bounds__(kWaves * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t table[];
+    uint8_t* smem = table + kTable;
+    fill_table(p.a, table);
     const int rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
     int first = blockIdx.x, light = kMost;  // the 256 x 64 tiles take experts with up to `light` tokens
-    if (HEAVY && (int64_t)count_chunks(p.a, TileLight::kNT, 0, kMost) * ceil_of(rows, TileLight::kMT) > kCUs) {
+    if (HEAVY && (int64_t)count_chunks(p.a, table, TileLight::kNT, 0, kMost) * ceil_of(rows, TileLight::kMT) > kCUs) {
         light = kLight;
-        const int chunks = count_chunks(p.a, TileLarge::kNT, kLight + 1, kMost);
+        const int chunks = count_chunks(p.a, table, TileLarge::kNT, kLight + 1, kMost);
         int64_t tiles = (int64_t)chunks * ceil_of(rows, TileLarge::kMT);
         const int64_t mid = (int64_t)chunks * ceil_of(rows, TileMid::kMT);
         if ((float)ceil_of(tiles, kCUs) * 2.1f < (float)ceil_of(mid, kCUs) * 1.27f) {
-            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, smem, kLight + 1, kMost, chunks, first);
+            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, table, smem, kLight + 1, kMost, chunks, first);
         } else {
-            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, smem, kLight + 1, kMost, chunks, first);
+            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, table, smem, kLight + 1, kMost, chunks, first);
             tiles = mid;
         }
         // the light tiles begin with the workgroup, of the same XCD, that the heavy ones' last round did not reach
         first = (int)((blockIdx.x + gridDim.x - (int64_t)ceil_of(tiles, kXCDs) * kXCDs % gridDim.x) % gridDim.x);
     }
-    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, smem, 0, light, count_chunks(p.a, TileLight::kNT, 0, light), first);
+    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, table, smem, 0, light, count_chunks(p.a, table, TileLight::kNT, 0, light), first);
 }
 
 template <int MODE, bool HEAVY>
 moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
     const int G = (MODE == kGateUp ? p.a.d : p.a.f) / 128, rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
-    const int lds = HEAVY ? std::max(TileLight::lds(G), std::max(TileLarge::lds(G), TileMid::lds(G))) : TileLight::lds(G);
+    const int lds = kTable + (HEAVY ? std::max(TileLight::lds(G), std::max(TileLarge::lds(G), TileMid::lds(G))) : TileLight::lds(G));
     auto kern = ffn_fp8_tile_kernel<MODE, HEAVY>;
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     const int64_t tiles = work_items(p.a, TileLight::kNT) * ((rows + TileLight::kMT - 1) / TileLight::kMT);
@@ -695,7 +714,7 @@ moe_status gemm_fp8_tile(const GemmFp8& g, const void* tile, hipStream_t st) {
 
 moe_status ffn_fp8_tile(const FfnFp8& p, int mode, hipStream_t st) {
     const int G = (mode == kGateUp ? p.a.d : p.a.f) / 128;
-    const bool heavy = p.a.T > kLight && TileLarge::lds(G) <= kLds && TileMid::lds(G) <= kLds;
+    const bool heavy = p.a.T > kLight && kTable + TileLarge::lds(G) <= kLds && kTable + TileMid::lds(G) <= kLds;
     if (mode == kGateUp)
         return heavy ? launch_ffn<kGateUp, true>(p, st, "ffn_fp8_gateup_tile")
                      : launch_ffn<kGateUp, false>(p, st, "ffn_fp8_gateup_tile");
