@@ -444,26 +444,80 @@ __device__ __forceinline__ float silu_mul_quick(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.442695041f)) * u;
 }
 
-// The experts' counts and slots in LDS, for up to kTableExperts (more are read from memory): a tile's item is then
-// found without waiting for memory, where a load waits behind the stores of the tile before.
-constexpr int kTableExperts = 256, kTable = 8 * kTableExperts;  // bytes
-__device__ __forceinline__ void fill_table(const FfnArgs& a, uint8_t* table) {
-    for (int e = threadIdx.x; e < min(a.E, kTableExperts); e += blockDim.x) {
-        ((int32_t*)table)[e] = a.counts[e];
-        ((int32_t*)table)[kTableExperts + e] = a.slot_of_expert[e];
+// The call's experts in LDS, for up to kTableExperts (more are read from memory): a tile's item is then found in some
+// hundred cycles, where loads wait behind the stores of the tile before and a scan over the counts takes 1.4 us.
+constexpr int kTableExperts = 256;
+struct Table {
+    int32_t count[kTableExperts], slot[kTableExperts], row[kTableExperts];  // row: the first sorted one
+    int32_t end[kTableExperts];  // chunks of the pass's experts up to and with this one
+};
+
+// every lane: inclusive sum over the lanes up to it
+__device__ __forceinline__ int lanes_sum(int v, int lane) {
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const int o = __shfl_up(v, s, 64);
+        if (lane >= s) v += o;
+    }
+    return v;
+}
+
+__device__ __forceinline__ void fill_table(const FfnArgs& a, Table& tb) {
+    if (a.E > kTableExperts) return;
+    for (int e = threadIdx.x; e < kTableExperts; e += blockDim.x) {
+        tb.count[e] = e < a.E ? a.counts[e] : 0;
+        tb.slot[e] = e < a.E ? a.slot_of_expert[e] : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int e = 4 * threadIdx.x;
+        const int4 c = *(const int4*)&tb.count[e];
+        const int first = lanes_sum(c.x + c.y + c.z + c.w, threadIdx.x) - (c.x + c.y + c.z + c.w);
+        *(int4*)&tb.row[e] = make_int4(first, first + c.x, first + c.x + c.y, first + c.x + c.y + c.z);
     }
     __syncthreads();
 }
 
-// The chunks of nt tokens of the experts that hold n_lo to n_hi (every lane gets the sum).
-__device__ __forceinline__ int count_chunks(const FfnArgs& a, const uint8_t* table, int nt, int n_lo, int n_hi) {
+// The chunks of nt tokens of the experts that hold n_lo to n_hi, the shared one's last (every lane gets the sum); with
+// `pass`, the table's ends for them too.
+__device__ __forceinline__ int count_chunks(const FfnArgs& a, Table& tb, int nt, int n_lo, int n_hi, bool pass) {
     auto chunks = [&](int n) { return n >= n_lo && n <= n_hi ? (n + nt - 1) / nt : 0; };
-    int c = 0;
-    for (int e = threadIdx.x & 63; e < a.E; e += 64)
-        c += chunks(e < kTableExperts ? ((const int32_t*)table)[e] : a.counts[e]);
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) c += __shfl_xor(c, s, 64);
-    return __builtin_amdgcn_readfirstlane(c) + (a.shared_w ? chunks(a.T) : 0);
+    const int lane = threadIdx.x & 63, shared = a.shared_w ? chunks(a.T) : 0;
+    if (a.E > kTableExperts) {
+        int c = 0;
+        for (int e = lane; e < a.E; e += 64) c += chunks(a.counts[e]);
+        return __shfl(lanes_sum(c, lane), 63, 64) + shared;
+    }
+    const int4 n = *(const int4*)&tb.count[4 * lane];
+    const int c0 = chunks(n.x), c1 = c0 + chunks(n.y), c2 = c1 + chunks(n.z), c3 = c2 + chunks(n.w);
+    const int last = lanes_sum(c3, lane), first = last - c3;
+    if (pass) {
+        __syncthreads();  // nobody reads the ends of the pass before any more
+        if (threadIdx.x < 64) *(int4*)&tb.end[4 * lane] = make_int4(first + c0, first + c1, first + c2, last);
+        __syncthreads();
+    }
+    return __builtin_amdgcn_readfirstlane(__shfl(last, 63, 64)) + shared;
+}
+
+// Work item `item` of the pass (it exists): as find_item
+__device__ __forceinline__ void find_in_table(const FfnArgs& a, const Table& tb, int nt, int item, int& e, int& chunk,
+                                              int& slot, int& n, int& p0) {
+    const int4 end = *(const int4*)&tb.end[4 * (threadIdx.x & 63)];
+    // the ends do not fall: as many experts end before the item as come before its own
+    const int at = __popcll(__ballot(end.x <= item)) + __popcll(__ballot(end.y <= item)) +
+                   __popcll(__ballot(end.z <= item)) + __popcll(__ballot(end.w <= item));
+    if (at >= kTableExperts) {
+        e = slot = -1;
+        n = a.T;
+        p0 = a.T * a.k;
+        chunk = item - __builtin_amdgcn_readfirstlane(tb.end[kTableExperts - 1]);
+        return;
+    }
+    e = at;
+    slot = __builtin_amdgcn_readfirstlane(tb.slot[at]);
+    n = __builtin_amdgcn_readfirstlane(tb.count[at]);
+    p0 = __builtin_amdgcn_readfirstlane(tb.row[at]);
+    chunk = item - (__builtin_amdgcn_readfirstlane(tb.end[at]) - (n + nt - 1) / nt);
 }
 
 // This workgroup's tiles of the experts that hold n_lo to n_hi tokens (chunks: their chunks of kNT).  Workgroup
@@ -471,7 +525,7 @@ __device__ __forceinline__ int count_chunks(const FfnArgs& a, const uint8_t* tab
 // weights or the same tokens share an L2 (2048 tokens, 8 of 128 experts of 2048 x 768: 254 -> 236 us against tiles
 // dealt out in turn, 8192 on 7 of 4096 x 2048: 1597 -> 1526).
 template <int MODE, int RA, int NTB, int NW, int RW, int RX>
-__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const uint8_t* table, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
+__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const Table& tb, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     static_assert(MODE != kGateUp || (RA % 2 == 0 && TL::kMT % 256 == 0), "gate/up tiles hold whole groups of h");
     const FfnArgs& a = p.a;
@@ -488,12 +542,8 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const uint8_t* table,
         const int lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), G = K / 128;
         const int bx = (int)(id % gx);
         int e, chunk, slot, n_all, p0;
-        const bool any = a.E <= kTableExperts
-                             ? find_work_slot<kTableExperts / 64>((const int32_t*)table, (const int32_t*)table + kTableExperts,
-                                                                  a.E, a.T, a.k, TL::kNT, a.shared_w != nullptr, (int)(id / gx),
-                                                                  e, chunk, slot, n_all, p0, n_lo, n_hi)
-                             : find_item(a, TL::kNT, (int)(id / gx), e, chunk, slot, n_all, p0, n_lo, n_hi);
-        if (!any) return;
+        if (a.E <= kTableExperts) find_in_table(a, tb, TL::kNT, (int)(id / gx), e, chunk, slot, n_all, p0);
+        else if (!find_item(a, TL::kNT, (int)(id / gx), e, chunk, slot, n_all, p0, n_lo, n_hi)) return;
         const bool shared = e == -1;
         const int nt = min(TL::kNT, n_all - chunk * TL::kNT);
         p0 += chunk * TL::kNT;  // first row of the tile
@@ -614,7 +664,7 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const uint8_t* table,
 //   compute units at 2.1 and 1.27 us a step (the dense product's costs): 384 tokens on each of 8 44 / 28 / 35,
 //   1000 on each of 8 50 / 55 / 53, 517 on each of 7 136 / 127 / 123, 4096 on each of 7 522 / 608 / 765.
 // HEAVY false: no expert of the call can hold more than kLight, or the larger tiles' scales exceed the LDS
-// (inputs beyond 11264).
+// (inputs beyond 10752).
 constexpr int kLight = 64, kMost = 1 << 30, kWaves = 8;
 typedef Tile8<4, 8, kWaves, 1, 3> TileLarge;
 typedef Tile8<2, 8, kWaves, 2, 3> TileMid;
@@ -624,32 +674,34 @@ typedef Tile8<2, 4, kWaves, 2, 4> TileLight;
 // the counts give is through (a launch for the most there could be took 19 to 58 us to find nothing).
 template <int MODE, bool HEAVY>
 __global__ __launch_bounds__(kWaves * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
-    extern __shared__ __align__(16) uint8_t table[];
-    uint8_t* smem = table + kTable;
-    fill_table(p.a, table);
+    extern __shared__ __align__(16) uint8_t lds[];
+    Table& tb = *(Table*)lds;
+    uint8_t* smem = lds + sizeof(Table);
+    fill_table(p.a, tb);
     const int rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
     int first = blockIdx.x, light = kMost;  // the 256 x 64 tiles take experts with up to `light` tokens
-    if (HEAVY && (int64_t)count_chunks(p.a, table, TileLight::kNT, 0, kMost) * ceil_of(rows, TileLight::kMT) > kCUs) {
+    if (HEAVY && (int64_t)count_chunks(p.a, tb, TileLight::kNT, 0, kMost, false) * ceil_of(rows, TileLight::kMT) > kCUs) {
         light = kLight;
-        const int chunks = count_chunks(p.a, table, TileLarge::kNT, kLight + 1, kMost);
+        const int chunks = count_chunks(p.a, tb, TileLarge::kNT, kLight + 1, kMost, true);
         int64_t tiles = (int64_t)chunks * ceil_of(rows, TileLarge::kMT);
         const int64_t mid = (int64_t)chunks * ceil_of(rows, TileMid::kMT);
         if ((float)ceil_of(tiles, kCUs) * 2.1f < (float)ceil_of(mid, kCUs) * 1.27f) {
-            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, table, smem, kLight + 1, kMost, chunks, first);
+            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, tb, smem, kLight + 1, kMost, chunks, first);
         } else {
-            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, table, smem, kLight + 1, kMost, chunks, first);
+            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, tb, smem, kLight + 1, kMost, chunks, first);
             tiles = mid;
         }
         // the light tiles begin with the workgroup, of the same XCD, that the heavy ones' last round did not reach
         first = (int)((blockIdx.x + gridDim.x - (int64_t)ceil_of(tiles, kXCDs) * kXCDs % gridDim.x) % gridDim.x);
     }
-    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, table, smem, 0, light, count_chunks(p.a, table, TileLight::kNT, 0, light), first);
+    const int chunks = count_chunks(p.a, tb, TileLight::kNT, 0, light, true);
+    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, tb, smem, 0, light, chunks, first);
 }
 
 template <int MODE, bool HEAVY>
 moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
     const int G = (MODE == kGateUp ? p.a.d : p.a.f) / 128, rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
-    const int lds = kTable + (HEAVY ? std::max(TileLight::lds(G), std::max(TileLarge::lds(G), TileMid::lds(G))) : TileLight::lds(G));
+    const int lds = (int)sizeof(Table) + (HEAVY ? std::max(TileLight::lds(G), std::max(TileLarge::lds(G), TileMid::lds(G))) : TileLight::lds(G));
     auto kern = ffn_fp8_tile_kernel<MODE, HEAVY>;
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     const int64_t tiles = work_items(p.a, TileLight::kNT) * ((rows + TileLight::kMT - 1) / TileLight::kMT);
@@ -714,7 +766,7 @@ moe_status gemm_fp8_tile(const GemmFp8& g, const void* tile, hipStream_t st) {
 
 moe_status ffn_fp8_tile(const FfnFp8& p, int mode, hipStream_t st) {
     const int G = (mode == kGateUp ? p.a.d : p.a.f) / 128;
-    const bool heavy = p.a.T > kLight && kTable + TileLarge::lds(G) <= kLds && kTable + TileMid::lds(G) <= kLds;
+    const bool heavy = p.a.T > kLight && (int)sizeof(Table) + TileLarge::lds(G) <= kLds && (int)sizeof(Table) + TileMid::lds(G) <= kLds;
     if (mode == kGateUp)
         return heavy ? launch_ffn<kGateUp, true>(p, st, "ffn_fp8_gateup_tile")
                      : launch_ffn<kGateUp, false>(p, st, "ffn_fp8_gateup_tile");
