@@ -16,7 +16,7 @@
 // written in 8 bits with its scale.
 //
 // Measured: 8192 x 4096 x 4096 in 131 us, 2.1 PFLOP/s; 8192 tokens on 6 of 256 experts of 4096 x 2048 and the shared
-// one, the six the same, 952 + 540 us, 1.9 PFLOP/s.  Counters of the first: the matrix cores are busy 56 % of the units'
+// one, the six the same, 905 + 505 us, 2.05 PFLOP/s.  Counters of the first: the matrix cores are busy 56 % of the units'
 // cycles (2.0 GHz under this load), the vector units about as much (four multiply-adds a product and one instruction
 // more), LDS 28 %, bank conflicts 3 % of that; the loop holds 32 products in 285 instructions.  What is left is two
 // waves a SIMD that both wait at a step's barrier and for operands one block ahead: the accumulators, 128 registers,
@@ -658,11 +658,11 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const Table& tb, uint
 // The tiles of a call (measured, us of the gate/up projection, 512 x 128 / 256 x 128 / 256 x 64 tiles, experts of
 // 2048 x 768 or, from 7 experts on, 4096 x 2048):
 // - All experts 256 rows x 64 tokens where each such tile has a compute unit of its own: 128 tokens on each of 8
-//   experts 44 / 29 / 21, 70 on each of 7 72 / 48 / 39.
+//   experts 36 / 26 / 20, 70 on each of 7 64 / 41 / 34.
 // - Else experts with up to kLight tokens take 256 x 64, with the weights two steps ahead (their weights' bytes
 //   bound them), and the others 512 x 128 or 256 x 128, whichever needs the less time for its rounds over the
-//   compute units at 2.1 and 1.27 us a step (the dense product's costs): 384 tokens on each of 8 44 / 28 / 35,
-//   1000 on each of 8 50 / 55 / 53, 517 on each of 7 136 / 127 / 123, 4096 on each of 7 522 / 608 / 765.
+//   compute units at 2.1 and 1.27 us a step (the dense product's costs): 384 tokens on each of 8 37 / 28 / 31,
+//   1000 on each of 8 43 / 49 / 49, 517 on each of 7 122 / 114 / 112, 4096 on each of 7 471 / 552 / 714.
 // HEAVY false: no expert of the call can hold more than kLight, or the larger tiles' scales exceed the LDS
 // (inputs beyond 10752).
 constexpr int kLight = 64, kMost = 1 << 30, kWaves = 8;
