@@ -61,12 +61,15 @@ __device__ __forceinline__ uint32_t quarter_max(uint32_t v) {
 // both, row l % 16 and the same 32 of the inputs, in the same order; result: token l % 16, rows
 // 4 (l / 16) .. + 3.
 //
-// The matrix core's e4m3 instructions align the products they add to the largest and drop what
-// falls below some 18 bits of it (measured: 1.5e-5 of the result on bell-shaped operands, the same
-// bits from the 32- and the 128-input forms).  mfma_fp8 is that: enough where the result is rounded
-// to bf16 or 8 bits, and twice the bf16 rate.  mfma_fp8_exact widens both operands to bf16 (exact) and
-// uses the bf16 instruction, whose sums are binary32 (5e-7 measured): where the weights' bytes bound
-// the product anyway, and where the caller wants a binary32 result.
+// The matrix core's e4m3 instructions cut the products of each run of 8 consecutive inputs off towards zero, below
+// 2^(E - 13), where 2^E is the largest product of two operands' powers of two in the run (2^-6 for a subnormal; zeros
+// do not count), and add the runs in binary32.  448 * 448 - 448 * 448 + 6 * 4 gives 0: E = 16, what lies below 8 is gone
+// (measured, the 32- and the 128-input forms alike).  A run of 8 is off by less than 2^(E - 10), so a sum of normal
+// operands by less than 2^-10 of the sum of its products' magnitudes; on bell-shaped operands by 1.5e-5 of the result.
+// mfma_fp8 is that, at twice the bf16 rate: taken where the sum is rounded to bf16 (half a step is 2^-8) and stored.
+// mfma_fp8_exact widens both operands to bf16 (exact) and uses the bf16 instruction, whose sums are binary32 (5e-7
+// measured): where the weights' bytes bound the product anyway, where the caller wants a binary32 result, and for
+// h, which is rounded to 8 bits and multiplied again.
 __device__ __forceinline__ f32x4_t mfma_fp8(i32x8_t a, i32x8_t b) {
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);

@@ -2,7 +2,7 @@
 //
 // A workgroup of NW waves computes MT = NW * RA * 16 weight rows x NT = 16 * NTB tokens; each wave owns RA
 // blocks of 16 rows for all of the tile's tokens.  Inputs advance 128 at a time, one scale group: a
-// step is one mfma_fp8 (fp8.h; mfma_fp8_exact where the caller wants binary32) per (row block, token
+// step is one mfma_fp8 (fp8.h; mfma_fp8_exact where the result is binary32 or h) per (row block, token
 // block), whose sum is added to binary32 accumulators times the token's scale and the row block's.
 //
 // Both operands go through LDS by direct-to-LDS loads: the tokens, which every wave reads, in a ring of
@@ -524,10 +524,11 @@ __device__ __forceinline__ void find_in_table(const FfnArgs& a, const Table& tb,
 // i runs on XCD i mod 8; each XCD takes a run of consecutive tiles, so that the tiles that read the same
 // weights or the same tokens share an L2 (2048 tokens, 8 of 128 experts of 2048 x 768: 254 -> 236 us against tiles
 // dealt out in turn, 8192 on 7 of 4096 x 2048: 1597 -> 1526).
-template <int MODE, int RA, int NTB, int NW, int RW, int RX>
-__device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const Table& tb, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
+template <int MODE, bool EXACT, int RA, int NTB, int NW, int RW, int RX>
+__device__ __forceinline__ void ffn_tiles(Tile8<RA, NTB, NW, RW, RX>, const FfnFp8& p, const Table& tb, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
     static_assert(MODE != kGateUp || (RA % 2 == 0 && TL::kMT % 256 == 0), "gate/up tiles hold whole groups of h");
+    static_assert(MODE != kGateUp || EXACT, "h from binary32 sums");
     const FfnArgs& a = p.a;
     const int nblk = MODE == kGateUp ? 2 * (a.f / 16) : a.d / 16;
     const int gx = (nblk + NW * RA - 1) / (NW * RA);  // tiles over the weight rows
@@ -584,7 +585,7 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const Table& tb, uint
         for (int u = 0; u < TL::kUnits; ++u)
             fd.x[u] = x + (size_t)source(8 * (wv * TL::kUnits + u) + (lane >> 3)) * K + 16 * chunk_of_lane(lane);
         f32x4_t acc[RA][NTB];
-        tile_loop<MODE, RA, NTB, NW, RW, RX, kWFrags, false, false>(
+        tile_loop<MODE, RA, NTB, NW, RW, RX, kWFrags, EXACT, false>(
             fd, smem, G, G, K, wv, lane, tid, [&](int t) { return x_scale + (size_t)source(t) * G; },
             [&](int s) {
                 // gate/up: the gate and the up scale of each 128 columns of h (16 blocks); down: of 8 blocks
@@ -648,61 +649,81 @@ __device__ __forceinline__ void ffn_tiles(const FfnFp8& p, const Table& tb, uint
                 };
                 store_rows<E>(acc, area, lane, RA * 16, true, row);
             };
-            if (a.y_bf16) rows((uint16_t*)a.y_perm);
-            else rows((float*)a.y_perm);
+            if constexpr (EXACT) rows((float*)a.y_perm);
+            else rows((uint16_t*)a.y_perm);
         }
         __syncthreads();  // the next tile's scales and magnitudes take the same LDS
     }
 }
 
-// The tiles of a call (measured, us of the gate/up projection, 512 x 128 / 256 x 128 / 256 x 64 tiles, experts of
-// 2048 x 768 or, from 7 experts on, 4096 x 2048):
-// - All experts 256 rows x 64 tokens where each such tile has a compute unit of its own: 128 tokens on each of 8
-//   experts 36 / 26 / 20, 70 on each of 7 64 / 41 / 34.
+// The tiles of a call.  The gate and up sums are binary32 (EXACT): h is rounded to 8 bits next, and what the e4m3
+// instruction drops would move elements across borders between two e4m3 values, whole rows by 1.3e-3 of their norm.
+// So are the down projection's where its rows are binary32; bf16 rows take the e4m3 instruction, as the dense product.
+//
+// EXACT: 512 x 64 or 256 x 64, whichever needs the less time for its rounds over the compute units at a cost of 7 to
+// 4.  Measured (us of the gate/up projection, 512 x 64 / 256 x 64 / 256 x 128): 64 tokens on each of 8 experts of
+// 2048 x 768 34 / 25 / 36, 517 38 / 47 / 40; 4096 x 2048, 128 on each of 7 60 / 44 / 63, 8192 1712 / 2162 / 1770;
+// popularity as 1 / rank^1.1, 6 of 256 of 4096 x 2048 and the shared one, 64 tokens 338 / 367 / 573, 2048 997 / 1164 /
+// 1442, 8192 2196 / 2713 / 2631.  (512 x 128 does not fit the registers: 64 of them hold the weights as bf16.)
+//
+// Else (bf16 rows of the down projection):
+// - All experts 256 rows x 64 tokens where each such tile has a compute unit of its own.
 // - Else experts with up to kLight tokens take 256 x 64, with the weights two steps ahead (their weights' bytes
 //   bound them), and the others 512 x 128 or 256 x 128, whichever needs the less time for its rounds over the
-//   compute units at 2.1 and 1.27 us a step (the dense product's costs): 384 tokens on each of 8 37 / 28 / 31,
-//   1000 on each of 8 43 / 49 / 49, 517 on each of 7 122 / 114 / 112, 4096 on each of 7 471 / 552 / 714.
+//   compute units at 2.1 and 1.27 us a step (the dense product's costs).
 // HEAVY false: no expert of the call can hold more than kLight, or the larger tiles' scales exceed the LDS
 // (inputs beyond 10752).
 constexpr int kLight = 64, kMost = 1 << 30, kWaves = 8;
 typedef Tile8<4, 8, kWaves, 1, 3> TileLarge;
 typedef Tile8<2, 8, kWaves, 2, 3> TileMid;
 typedef Tile8<2, 4, kWaves, 2, 4> TileLight;
+typedef Tile8<4, 4, kWaves, 1, 3> TileWide;
 
 // The grid is at most one workgroup a compute unit; each takes every gridDim.x-th tile until the work that
 // the counts give is through (a launch for the most there could be took 19 to 58 us to find nothing).
-template <int MODE, bool HEAVY>
+template <int MODE, bool EXACT, bool HEAVY>
 __global__ __launch_bounds__(kWaves * 64, 2) void ffn_fp8_tile_kernel(FfnFp8 p) {
     extern __shared__ __align__(16) uint8_t lds[];
     Table& tb = *(Table*)lds;
     uint8_t* smem = lds + sizeof(Table);
     fill_table(p.a, tb);
     const int rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
-    int first = blockIdx.x, light = kMost;  // the 256 x 64 tiles take experts with up to `light` tokens
-    if (HEAVY && (int64_t)count_chunks(p.a, tb, TileLight::kNT, 0, kMost, false) * ceil_of(rows, TileLight::kMT) > kCUs) {
-        light = kLight;
-        const int chunks = count_chunks(p.a, tb, TileLarge::kNT, kLight + 1, kMost, true);
-        int64_t tiles = (int64_t)chunks * ceil_of(rows, TileLarge::kMT);
-        const int64_t mid = (int64_t)chunks * ceil_of(rows, TileMid::kMT);
-        if ((float)ceil_of(tiles, kCUs) * 2.1f < (float)ceil_of(mid, kCUs) * 1.27f) {
-            ffn_tiles<MODE, 4, 8, kWaves, 1, 3>(p, tb, smem, kLight + 1, kMost, chunks, first);
-        } else {
-            ffn_tiles<MODE, 2, 8, kWaves, 2, 3>(p, tb, smem, kLight + 1, kMost, chunks, first);
-            tiles = mid;
+    if constexpr (EXACT) {
+        static_assert(TileWide::kNT == TileLight::kNT, "the same chunks");
+        const int chunks = count_chunks(p.a, tb, TileWide::kNT, 0, kMost, true);
+        const int64_t wide = ceil_of(chunks * ceil_of(rows, TileWide::kMT), kCUs);
+        const int64_t light = ceil_of(chunks * ceil_of(rows, TileLight::kMT), kCUs);
+        if (7 * wide < 4 * light) ffn_tiles<MODE, true>(TileWide{}, p, tb, smem, 0, kMost, chunks, blockIdx.x);
+        else ffn_tiles<MODE, true>(TileLight{}, p, tb, smem, 0, kMost, chunks, blockIdx.x);
+    } else {
+        int first = blockIdx.x, light = kMost;  // the 256 x 64 tiles take experts with up to `light` tokens
+        if (HEAVY && (int64_t)count_chunks(p.a, tb, TileLight::kNT, 0, kMost, false) * ceil_of(rows, TileLight::kMT) > kCUs) {
+            light = kLight;
+            const int chunks = count_chunks(p.a, tb, TileLarge::kNT, kLight + 1, kMost, true);
+            int64_t tiles = (int64_t)chunks * ceil_of(rows, TileLarge::kMT);
+            const int64_t mid = (int64_t)chunks * ceil_of(rows, TileMid::kMT);
+            if ((float)ceil_of(tiles, kCUs) * 2.1f < (float)ceil_of(mid, kCUs) * 1.27f) {
+                ffn_tiles<MODE, false>(TileLarge{}, p, tb, smem, kLight + 1, kMost, chunks, first);
+            } else {
+                ffn_tiles<MODE, false>(TileMid{}, p, tb, smem, kLight + 1, kMost, chunks, first);
+                tiles = mid;
+            }
+            // the light tiles begin with the workgroup, of the same XCD, that the heavy ones' last round did not reach
+            first = (int)((blockIdx.x + gridDim.x - (int64_t)ceil_of(tiles, kXCDs) * kXCDs % gridDim.x) % gridDim.x);
         }
-        // the light tiles begin with the workgroup, of the same XCD, that the heavy ones' last round did not reach
-        first = (int)((blockIdx.x + gridDim.x - (int64_t)ceil_of(tiles, kXCDs) * kXCDs % gridDim.x) % gridDim.x);
+        const int chunks = count_chunks(p.a, tb, TileLight::kNT, 0, light, true);
+        ffn_tiles<MODE, false>(TileLight{}, p, tb, smem, 0, light, chunks, first);
     }
-    const int chunks = count_chunks(p.a, tb, TileLight::kNT, 0, light, true);
-    ffn_tiles<MODE, 2, 4, kWaves, 2, 4>(p, tb, smem, 0, light, chunks, first);
 }
 
-template <int MODE, bool HEAVY>
+template <int MODE, bool EXACT, bool HEAVY>
 moe_status launch_ffn(const FfnFp8& p, hipStream_t st, const char* name) {
     const int G = (MODE == kGateUp ? p.a.d : p.a.f) / 128, rows = MODE == kGateUp ? 2 * p.a.f : p.a.d;
-    const int lds = (int)sizeof(Table) + (HEAVY ? std::max(TileLight::lds(G), std::max(TileLarge::lds(G), TileMid::lds(G))) : TileLight::lds(G));
-    auto kern = ffn_fp8_tile_kernel<MODE, HEAVY>;
+    int lds = TileLight::lds(G);
+    if (EXACT) lds = std::max(lds, TileWide::lds(G));
+    if (HEAVY) lds = std::max(lds, std::max(TileLarge::lds(G), TileMid::lds(G)));
+    lds += (int)sizeof(Table);
+    auto kern = ffn_fp8_tile_kernel<MODE, EXACT, HEAVY>;
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     const int64_t tiles = work_items(p.a, TileLight::kNT) * ((rows + TileLight::kMT - 1) / TileLight::kMT);
     ProfScope sc(name, st);
@@ -765,12 +786,12 @@ moe_status gemm_fp8_tile(const GemmFp8& g, const void* tile, hipStream_t st) {
 }
 
 moe_status ffn_fp8_tile(const FfnFp8& p, int mode, hipStream_t st) {
-    const int G = (mode == kGateUp ? p.a.d : p.a.f) / 128;
+    if (mode == kGateUp) return launch_ffn<kGateUp, true, false>(p, st, "ffn_fp8_gateup_tile");
+    if (!p.a.y_bf16) return launch_ffn<kDown, true, false>(p, st, "ffn_fp8_down_tile");
+    const int G = p.a.f / 128;
     const bool heavy = p.a.T > kLight && (int)sizeof(Table) + TileLarge::lds(G) <= kLds && (int)sizeof(Table) + TileMid::lds(G) <= kLds;
-    if (mode == kGateUp)
-        return heavy ? launch_ffn<kGateUp, true>(p, st, "ffn_fp8_gateup_tile")
-                     : launch_ffn<kGateUp, false>(p, st, "ffn_fp8_gateup_tile");
-    return heavy ? launch_ffn<kDown, true>(p, st, "ffn_fp8_down_tile") : launch_ffn<kDown, false>(p, st, "ffn_fp8_down_tile");
+    return heavy ? launch_ffn<kDown, false, true>(p, st, "ffn_fp8_down_tile")
+                 : launch_ffn<kDown, false, false>(p, st, "ffn_fp8_down_tile");
 }
 
 }  // namespace moe

@@ -189,9 +189,11 @@ MOE_API moe_status moe_route_permute(const void* x, moe_dtype act, int T, int d,
  * Intermediate h is rounded to bf16 when act is BF16 (binary32 when act is F32).
  * Weights FP8_B128 need act BF16: each row of x is quantised (see FP8 above), the gate and up sums
  * are of 8-bit products, h is quantised from its binary32 values and the down projection's products
- * are of 8-bit values again: bitwise what moe_quant_fp8 and moe_expert_ffn_fp8 give.  Calls of up to
- * 16 tokens sum in binary32; above, a 128-input group's sum is the matrix core's own (see
- * moe_gemm_fp8), so a token's row may differ in its last bits between the two. */
+ * are of 8-bit values again: bitwise what moe_quant_fp8 and moe_expert_ffn_fp8 give.  Sums are
+ * binary32, but for the down projection of calls above 16 tokens into BF16 rows, which are summed as
+ * the BF16 results of moe_gemm_fp8.  The order of the sums differs between calls of up to 16 tokens and
+ * longer ones: an element of h that lies on a border between two e4m3 values to within it may take the
+ * other one, which moves a token's row by some 2e-4 of its norm. */
 #define MOE_SLOT_ELSEWHERE (-2)
 /* Above 64 tokens (prefill) the experts run on the matrix-core grouped GEMM, which feeds int4
  * weights to the matrix cores as bf16(q * s).  Experts holding at most moe_prefill_gemv_tokens(w)

@@ -394,6 +394,73 @@ def test_layer_with_fp8_experts(moe, shape, T):
     assert np.array_equal(_bits(y16), _bits(b))
 
 
+def _experts_of(moe, d, f, wg, wu, wd, sg, su, sd):
+    """One expert of the given e4m3 values and block scales as a pool of one slot."""
+    import torch
+
+    img = moe.pack_expert("fp8", d, f, synth.e4m3_bits(wg), synth.e4m3_bits(wu), synth.e4m3_bits(wd),
+                          *[np.asarray(v, np.float32) for v in (sg, su, sd)])
+    return torch.from_numpy(img).cuda(), img.nbytes
+
+
+def _one_expert_call(moe, row, T, d, f, pool, stride, y_dtype):
+    """T copies of an e4m3 row (scales 1) through the pool's only expert."""
+    import torch
+
+    x = torch.from_numpy(np.repeat(synth.e4m3_bits(row[None]), T, 0)).cuda().view(torch.float8_e4m3fn)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    out, _ = moe.expert_ffn_fp8(x, torch.ones(T, d // 128, device="cuda"),
+                                torch.arange(T, dtype=torch.int32, device="cuda"), i32([0, T]), i32([T]), i32([0]),
+                                pool, 1, stride, f, 1, y_dtype=y_dtype)
+    return out
+
+
+# 448 * 448 - 448 * 448 + 6 * 4: eight inputs, the rest zeros.  Sums in binary32: 24 within (8 + 4) u M, eight
+# products and a group's term, M = 2 * 448^2 + 24: 1.2 % of it.  The e4m3 instructions give 0.
+CANCEL, CANCEL_TOL = 24.0, 0.012
+
+
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+@pytest.mark.parametrize("d,f,T", [(128, 128, 16), (128, 128, 17), (256, 128, 130), (128, 16384, 200)])
+def test_gate_and_up_sums_are_binary32(moe, d, f, T, y):
+    """Two large products that cancel leave the small ones beside them, streamed and in either tile.
+
+    silu(g) u moves by at most 2.3 times the sums' 1.2 % (u once, g by 1 + g (1 - sigma(g)) <= 1.28 times): 2.8 %.
+    The largest of a group is 448 s, so equal h carry no rounding to 8 bits; the down projection adds f equal terms
+    (128 u each of them) and bf16 rounds once: 3.5 % holds all of it."""
+    import torch
+
+    row = np.zeros(d)
+    row[:8] = [448.0, 448.0] + 6 * [4.0]
+    wg = np.ones((f, d))
+    wg[:, 0], wg[:, 1] = 448.0, -448.0
+    sg = np.full((f // 128, d // 128), 2.0 ** -4)
+    pool, stride = _experts_of(moe, d, f, wg, wg, np.ones((d, f)), sg, sg, np.full((d // 128, f // 128), 1.0 / f))
+    got = y_to_f64(_one_expert_call(moe, row, T, d, f, pool, stride, torch.float32 if y == "f32" else torch.bfloat16))
+    g = CANCEL * 2.0 ** -4
+    want = g / (1 + np.exp(-g)) * g
+    assert (np.abs(got - want) <= 0.035 * want).all(), (got.min(), got.max(), want)
+
+
+@pytest.mark.parametrize("d,f,T", [(128, 128, 16), (128, 128, 17), (128, 256, 130), (8192, 128, 600)])
+def test_down_sums_are_binary32_where_the_rows_are(moe, d, f, T):
+    """The same in the down projection into binary32 rows: h_0 = h_1 = 112 h_i, 448 and 4 in 8 bits.  h is one
+    product, exact to a few u, and 1.2 % is the sums' again."""
+    import torch
+
+    row = np.zeros(d)
+    row[0] = 1.0
+    wg, wu, wd = np.zeros((f, d)), np.zeros((f, d)), np.ones((d, f))
+    wg[:, 0], wu[:8, 0], wu[:2, 0] = 2.0, 2.0 ** -4, 7.0
+    wd[:, 0], wd[:, 1] = 448.0, -448.0
+    gu, down = np.ones((f // 128, d // 128)), np.ones((d // 128, f // 128))
+    pool, stride = _experts_of(moe, d, f, wg, wu, wd, gu, gu, down)
+    out = _one_expert_call(moe, row, T, d, f, pool, stride, torch.float32)
+    want = 6 * 2.0 / (1 + np.exp(-2.0)) * 2.0 ** -4
+    got = y_to_f64(out)
+    assert (np.abs(got - want) <= (CANCEL_TOL + 1e-4) * want).all(), (got.min(), got.max(), want)
+
+
 @pytest.mark.parametrize("T", [3, 40, 200])
 def test_expert_chosen_twice_and_shared_slots(moe, T):
     """A token that chose one expert twice gets its row twice; experts that share a slot give the same rows."""
