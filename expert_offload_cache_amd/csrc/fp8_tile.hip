@@ -438,12 +438,6 @@ moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
 // ---- the routed experts' projections ------------------------------------------------------------------
 __device__ __forceinline__ int64_t ceil_of(int64_t n, int block) { return (n + block - 1) / block; }
 
-// g / (1 + e^-g) * u by the hardware's exponential and reciprocal (within an ulp each; the exponent's rounding adds
-// |g| 2^-24): h is rounded to 8 bits next.  A tile has 64 of them a lane, which took 6 us with the exact quotient.
-__device__ __forceinline__ float silu_mul_quick(float g, float u) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.442695041f)) * u;
-}
-
 // The call's experts in LDS, for up to kTableExperts (more are read from memory): a tile's item is then found in some
 // hundred cycles, where loads wait behind the stores of the tile before and a scan over the counts takes 1.4 us.
 constexpr int kTableExperts = 256;
@@ -605,7 +599,7 @@ __device__ __forceinline__ void ffn_tiles(Tile8<RA, NTB, NW, RW, RX>, const FfnF
                 for (int i = 0; i < RA / 2; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float h = silu_mul_quick(acc[2 * i][j][c], acc[2 * i + 1][j][c]);
+                        const float h = silu_mul(acc[2 * i][j][c], acc[2 * i + 1][j][c]);
                         acc[2 * i][j][c] = h;
                         m = umax(m, abs_bits(h));
                     }

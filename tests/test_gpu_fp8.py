@@ -461,6 +461,31 @@ def test_down_sums_are_binary32_where_the_rows_are(moe, d, f, T):
     assert (np.abs(got - want) <= (CANCEL_TOL + 1e-4) * want).all(), (got.min(), got.max(), want)
 
 
+@pytest.mark.parametrize("d,f,T", [(128, 128, 16), (128, 128, 17), (128, 16384, 200)])
+def test_swiglu_to_binary32(moe, d, f, T):
+    """One element of h a token, so 448 of its scale, read back through a binary32 row: silu(g) |g| for g from -87 to 87.
+    The exponential is within 2 u (its relative error is the quotient's at most), 1 + e^-g, the quotient and the
+    product 1 u each, the scale 1 u, its product with the weights' 1 u, subnormal results 2^-149 more: 16 u."""
+    import torch
+
+    rng = np.random.default_rng(T)
+    g = np.concatenate([np.linspace(-87, 87, T // 2), rng.uniform(-87, -1, T - T // 2)]).astype(np.float32)
+    wg, wu, wd = np.zeros((f, d)), np.zeros((f, d)), np.zeros((d, f))
+    wg[0, 0], wu[0, 1], wd[:, 0] = 1.0, 1.0, 1.0
+    gu, down = np.ones((f // 128, d // 128)), np.ones((d // 128, f // 128))
+    pool, stride = _experts_of(moe, d, f, wg, wu, wd, gu, gu, down)
+    rows = np.zeros((T, d))
+    rows[:, 0], rows[:, 1] = np.sign(g), 1.0
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    out, _ = moe.expert_ffn_fp8(torch.from_numpy(synth.e4m3_bits(rows)).cuda().view(torch.float8_e4m3fn),
+                                torch.from_numpy(np.abs(g)[:, None]).cuda(), i32(list(range(T))), i32([0, T]), i32([T]),
+                                i32([0]), pool, 1, stride, f, 1)
+    g = g.astype(np.float64)
+    want = g / (1 + np.exp(-g)) * np.abs(g)
+    err = np.abs(y_to_f64(out) - want[:, None])
+    assert (err <= 16 * U * np.abs(want)[:, None] + 2.0 ** -149).all(), (err / np.abs(want)[:, None]).max() / U
+
+
 @pytest.mark.parametrize("T", [3, 40, 200])
 def test_expert_chosen_twice_and_shared_slots(moe, T):
     """A token that chose one expert twice gets its row twice; experts that share a slot give the same rows."""
