@@ -238,6 +238,46 @@ def test_product(moe, M, N, K, out):
     _check_product(ops, c, fast=out == "bf16")
 
 
+@pytest.mark.parametrize("M,N,K", [(20, 256, 384), (300, 512, 768), (1000, 1024, 2000), (2048, 2048, 1024), (2048, 8192, 384)])
+def test_bf16_product_of_outliers_and_small_values(moe, M, N, K):
+    """bf16 results of operands whose products in a run of 8 inputs span the type's range and cancel.
+
+    The e4m3 instructions cut each of a run's products off below 2^(E - 13) (fp8.h): less than 8 * 2^(E - 13) a run,
+    E the run's largest sum of two exponents, -6 for subnormals, zeros aside.  With the binary32 roundings of the
+    groups' terms, (K + 4 G) u M, and the result's own, 2^-8 of it, that bounds every element; a binary32 result stays
+    within the roundings alone."""
+    import torch
+
+    rng = np.random.default_rng([M, N, K])
+    G = -(-K // 128)
+
+    def operand(R, sign):  # magnitudes from 2^-9 to 448 in a row, some zeros; a run's second value is sign times its first
+        v = rng.choice([-1.0, 1.0], (R, K)) * 2.0 ** rng.integers(-9, 9, (R, K)) * (1 + rng.integers(0, 7, (R, K)) / 8)
+        v[rng.random((R, K)) < 0.1] = 0.0
+        v[:, 1::8] = sign * v[:, ::8]
+        return synth.e4m3_bits(np.clip(v, -448, 448))
+
+    a, w = operand(M, 1), operand(N, -1)
+    sa = rng.uniform(0.5, 2, (M, G)).astype(np.float32)
+    sw = rng.uniform(0.5, 2, (-(-N // 128), G)).astype(np.float32)
+    dev = [torch.from_numpy(t).cuda() for t in (a, sa, w, sw)]
+    dev[0], dev[2] = dev[0].view(torch.float8_e4m3fn), dev[2].view(torch.float8_e4m3fn)
+    rows, cols = rng.integers(0, M, 12), rng.integers(0, N, 40)
+    A, W = fp8.decode(a[rows]), fp8.decode(w[cols])
+    ex = lambda v: np.where(v == 0, -99, np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6)))).astype(int)
+    E = (ex(A)[:, None, :] + ex(W)[None, :, :]).reshape(12, 40, K // 8, 8).max(3)
+    cut = np.where(E > -50, 8 * 2.0 ** (E - 13.0), 0.0)
+    cut = np.pad(cut, [(0, 0), (0, 0), (0, 16 * G - K // 8)]).reshape(12, 40, G, 16).sum(3)
+    s = sa[rows].astype(np.float64)[:, None, :] * sw[cols // 128].astype(np.float64)[None]
+    Av, Wv = fp8.rows_value(A, sa[rows].astype(np.float64)), fp8.rows_value(W, sw[cols // 128].astype(np.float64))
+    ref, mag = Av @ Wv.T, np.abs(Av) @ np.abs(Wv).T
+    at = (torch.from_numpy(rows).cuda()[:, None], torch.from_numpy(cols).cuda()[None])
+    sums = (K + 4 * G) * U * mag
+    err = np.abs(y_to_f64(moe.gemm_fp8(*dev)[at]) - ref)
+    assert (err <= (1 + 2.0 ** -8) * (sums + (cut * s).sum(2)) + 2.0 ** -8 * np.abs(ref)).all()
+    assert (np.abs(y_to_f64(moe.gemm_fp8(*dev, out_dtype=torch.float32)[at]) - ref) <= sums).all()
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 150, 700])
 def test_product_strides(moe, M):
     """Wider rows (their rest NaN), a result inside a wider matrix at an odd element, and nothing written
