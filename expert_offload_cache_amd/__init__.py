@@ -202,6 +202,24 @@ def _dense(name, t, shape, dtype) -> None:
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
+def _expert_tensors(T, d, f, E, k, wdt, perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
+                    y_perm) -> None:
+    """Checks that the kernels of a grouped expert call stay inside its tensors (the library has their addresses alone)."""
+    i32 = _torch().int32
+    for name, t, n in (("perm", perm, T * k), ("offsets", offsets, E + 1), ("counts", counts, E),
+                       ("slot_of_expert", slot_of_expert, E)):
+        if t.dtype != i32 or t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int32 of {n} elements at least, got {t.dtype} {list(t.shape)}")
+    rows = T * k + (T if shared_w is not None else 0)
+    _y_code(y_perm)
+    if y_perm.numel() < rows * d or not y_perm.is_contiguous():
+        raise ValueError(f"y_perm must be contiguous and hold {rows} rows of {d}, got {list(y_perm.shape)}")
+    slot = slot_bytes(d, f, wdt)
+    for name, t, n in (("slot_pool", slot_pool, (n_slots - 1) * slot_stride + slot), ("shared_w", shared_w, slot)):
+        if t is not None and (t.numel() * t.element_size() < n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous and hold {n} bytes, got {t.dtype} {list(t.shape)}")
+
+
 def _quantised_out(x, shape, q, scale):
     """The given (or new) e4m3 rows and scales of `shape` -> (q, scale, elements from a row of q to the next)."""
     torch = _torch()
@@ -303,7 +321,8 @@ def expert_ffn_fp8(x, x_scale, perm, offsets, counts, slot_of_expert, slot_pool,
     if ws is None:
         ws = torch.zeros(workspace_bytes(T, d, f, E, k, shared_w is not None, MOE_BF16, MOE_FP8_B128),
                          dtype=torch.uint8, device=x.device)
-    _contig(perm, offsets, counts, slot_of_expert, y_perm)
+    _expert_tensors(T, d, f, E, k, "fp8", perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
+                    y_perm)
     _on_current_device(x, x_scale, perm, offsets, counts, slot_of_expert, slot_pool, shared_w, y_perm, ws)
     check(lib().moe_expert_ffn_fp8(_p(x), _p(x_scale), T, d, f, E, k, _p(perm), _p(offsets), _p(counts),
                                    _p(slot_of_expert), n_slots, _p(slot_pool), slot_stride, _p(shared_w), _p(y_perm),

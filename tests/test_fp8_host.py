@@ -223,3 +223,43 @@ def test_binding_refusals(moe):
         moe.gemm_fp8(q, s, q, torch.zeros(1, 1), out_dtype=torch.float16)
     with pytest.raises(ValueError, match="out is"):
         moe.gemm_fp8(q, s, q, torch.zeros(1, 1), out_dtype=torch.float32, out=torch.zeros(4, 4, dtype=torch.bfloat16))
+
+
+def _grouped_tensors(moe, wdt, T=4, d=128, f=128, E=3, k=2):
+    """Host tensors of the right types and sizes for a grouped expert call with a shared expert, no longer than needed."""
+    import torch
+
+    slot = moe.slot_bytes(d, f, wdt)
+    i32 = dict(dtype=torch.int32)
+    return dict(perm=torch.zeros(T * k, **i32), offsets=torch.zeros(E + 1, **i32), counts=torch.zeros(E, **i32),
+                slot_of_expert=torch.zeros(E, **i32), slot_pool=torch.zeros(2 * slot + 256, dtype=torch.uint8), n_slots=2,
+                slot_stride=slot + 256, f=f, k=k, shared_w=torch.zeros(slot, dtype=torch.uint8),
+                y_perm=torch.zeros(T * k + T, d))
+
+
+def _wrong_sizes(good):
+    """(argument, tensor too short or of another type) for each tensor of a grouped expert call."""
+    import torch
+
+    for name in ("perm", "offsets", "counts", "slot_of_expert"):
+        yield name, good[name].long()
+    for name in ("perm", "offsets", "slot_of_expert", "slot_pool", "shared_w"):
+        yield name, good[name][:-1]
+    yield "y_perm", good["y_perm"][:-1]
+    yield "y_perm", good["y_perm"][:, :-1].contiguous()
+    yield "slot_pool", torch.zeros(2, 2 * good["slot_pool"].numel(), dtype=torch.uint8)[:, ::2]
+
+
+def test_expert_tensors_that_the_kernels_would_pass_the_end_of(moe):
+    """The binding knows the tensors' sizes, the library only their addresses: what is too short is refused."""
+    import torch
+
+    x, xs = torch.zeros(4, 128, dtype=torch.float8_e4m3fn), torch.zeros(4, 1)
+    good = _grouped_tensors(moe, "fp8")
+    with pytest.raises(ValueError, match="current GPU"):  # nothing wrong but where they live
+        moe.expert_ffn_fp8(x, xs, **good)
+    for name, t in _wrong_sizes(good):
+        with pytest.raises(ValueError, match=name):
+            moe.expert_ffn_fp8(x, xs, **dict(good, **{name: t}))
+    with pytest.raises(TypeError, match="y_perm"):
+        moe.expert_ffn_fp8(x, xs, **dict(good, y_perm=good["y_perm"].half()))
