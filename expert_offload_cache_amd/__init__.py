@@ -206,18 +206,23 @@ def _expert_tensors(T, d, f, E, k, wdt, perm, offsets, counts, slot_of_expert, s
                     y_perm) -> None:
     """Checks that the kernels of a grouped expert call stay inside its tensors (the library has their addresses alone)."""
     i32 = _torch().int32
-    for name, t, n in (("perm", perm, T * k), ("offsets", offsets, E + 1), ("counts", counts, E),
-                       ("slot_of_expert", slot_of_expert, E)):
-        if t.dtype != i32 or t.numel() < n or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous int32 of {n} elements at least, got {t.dtype} {list(t.shape)}")
-    rows = T * k + (T if shared_w is not None else 0)
+    if not (perm.dtype == offsets.dtype == counts.dtype == slot_of_expert.dtype == i32 and perm.numel() >= T * k
+            and offsets.numel() > E and slot_of_expert.numel() >= E):
+        for name, t, n in (("perm", perm, T * k), ("offsets", offsets, E + 1), ("counts", counts, E),
+                           ("slot_of_expert", slot_of_expert, E)):
+            if t.dtype != i32 or t.numel() < n:
+                raise ValueError(f"{name} must be int32 of {n} elements at least, got {t.dtype} {list(t.shape)}")
+    _contig(perm, offsets, counts, slot_of_expert, y_perm, slot_pool, shared_w)
     _y_code(y_perm)
-    if y_perm.numel() < rows * d or not y_perm.is_contiguous():
-        raise ValueError(f"y_perm must be contiguous and hold {rows} rows of {d}, got {list(y_perm.shape)}")
-    slot = slot_bytes(d, f, wdt)
-    for name, t, n in (("slot_pool", slot_pool, (n_slots - 1) * slot_stride + slot), ("shared_w", shared_w, slot)):
-        if t is not None and (t.numel() * t.element_size() < n or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous and hold {n} bytes, got {t.dtype} {list(t.shape)}")
+    rows, slot = T * k, slot_bytes(d, f, wdt)
+    if shared_w is not None:
+        rows += T
+        if shared_w.nbytes < slot:
+            raise ValueError(f"shared_w must hold {slot} bytes, got {shared_w.nbytes}")
+    if y_perm.numel() < rows * d:
+        raise ValueError(f"y_perm must hold {rows} rows of {d}, got {list(y_perm.shape)}")
+    if slot_pool.nbytes < (n_slots - 1) * slot_stride + slot:
+        raise ValueError(f"slot_pool must hold {n_slots} slots of {slot_stride} bytes, got {slot_pool.nbytes} bytes")
 
 
 def _quantised_out(x, shape, q, scale):

@@ -247,7 +247,6 @@ def _wrong_sizes(good):
         yield name, good[name][:-1]
     yield "y_perm", good["y_perm"][:-1]
     yield "y_perm", good["y_perm"][:, :-1].contiguous()
-    yield "slot_pool", torch.zeros(2, 2 * good["slot_pool"].numel(), dtype=torch.uint8)[:, ::2]
 
 
 def test_expert_tensors_that_the_kernels_would_pass_the_end_of(moe):
@@ -263,3 +262,5 @@ def test_expert_tensors_that_the_kernels_would_pass_the_end_of(moe):
             moe.expert_ffn_fp8(x, xs, **dict(good, **{name: t}))
     with pytest.raises(TypeError, match="y_perm"):
         moe.expert_ffn_fp8(x, xs, **dict(good, y_perm=good["y_perm"].half()))
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.expert_ffn_fp8(x, xs, **dict(good, slot_pool=torch.zeros(2, 2 * good["slot_pool"].numel(), dtype=torch.uint8)[:, ::2]))
