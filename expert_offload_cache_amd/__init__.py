@@ -140,19 +140,44 @@ def workspace_bytes(T, d, f, E, k, has_shared, act: int, wdt: int) -> int:
     return int(lib().moe_workspace_bytes(T, d, f, E, k, int(bool(has_shared)), act, wdt))
 
 
+def _expert_tensors(T, d, f, E, k, wdt, perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
+                    y_perm) -> None:
+    """Checks that the kernels of a grouped expert call stay inside its tensors (the library has their addresses alone)."""
+    i32 = _torch().int32
+    if not (perm.dtype == offsets.dtype == counts.dtype == slot_of_expert.dtype == i32 and perm.numel() >= T * k
+            and offsets.numel() > E and slot_of_expert.numel() >= E):
+        for name, t, n in (("perm", perm, T * k), ("offsets", offsets, E + 1), ("counts", counts, E),
+                           ("slot_of_expert", slot_of_expert, E)):
+            if t.dtype != i32 or t.numel() < n:
+                raise ValueError(f"{name} must be int32 of {n} elements at least, got {t.dtype} {list(t.shape)}")
+    _contig(perm, offsets, counts, slot_of_expert, y_perm, slot_pool, shared_w)
+    _y_code(y_perm)
+    rows, slot = T * k, slot_bytes(d, f, wdt)
+    if shared_w is not None:
+        rows += T
+        if shared_w.nbytes < slot:
+            raise ValueError(f"shared_w must hold {slot} bytes, got {shared_w.nbytes}")
+    if y_perm.numel() < rows * d:
+        raise ValueError(f"y_perm must hold {rows} rows of {d}, got {list(y_perm.shape)}")
+    if slot_pool.nbytes < (n_slots - 1) * slot_stride + slot:
+        raise ValueError(f"slot_pool must hold {n_slots} slots of {slot_stride} bytes, got {slot_pool.nbytes} bytes")
+
+
 def expert_ffn_grouped(x, perm, offsets, counts, slot_of_expert, slot_pool, n_slots: int, slot_stride: int,
                        wdt: str, f: int, k: int, shared_w=None, y_perm=None, ws=None, stream=None, y_dtype=None):
     """Grouped SwiGLU experts through the slot table. -> (y_perm [T*k (+T), d], ws).  y_perm's element
     type is that of the given tensor (float32, or bfloat16 with bf16 activations), else y_dtype
     (a torch dtype, default float32)."""
     torch = _torch()
-    _contig(x, perm, offsets, counts, slot_of_expert)
+    _contig(x)
     T, d = x.shape
     E = counts.shape[0]
     act = _act(x)
     rows = T * k + (T if shared_w is not None else 0)
     if y_perm is None:
         y_perm = torch.empty((rows, d), dtype=y_dtype or torch.float32, device=x.device)
+    _expert_tensors(T, d, f, E, k, wdt, perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
+                    y_perm)
     if ws is None:
         need = workspace_bytes(T, d, f, E, k, shared_w is not None, act, WDT[wdt])
         ws = torch.zeros(need, dtype=torch.uint8, device=x.device)
@@ -167,9 +192,13 @@ def expert_ffn_grouped_noalloc(x, perm, offsets, counts, slot_of_expert, slot_po
                                stream=None):
     """expert_ffn_grouped through moe_expert_ffn_grouped_noalloc: no workspace, the library's
     per-GPU scratch instead; y_perm must be given.  status: device int32 tensor or None."""
-    _contig(x, perm, offsets, counts, slot_of_expert, y_perm)
+    _contig(x)
     T, d = x.shape
     E = counts.shape[0]
+    _expert_tensors(T, d, f, E, k, wdt, perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
+                    y_perm)
+    if status is not None and (status.dtype != _torch().int32 or status.numel() < 1):
+        raise ValueError(f"status must be an int32 tensor, got {status.dtype} {list(status.shape)}")
     check(lib().moe_expert_ffn_grouped_noalloc(_p(x), _act(x), T, d, f, E, k, _p(perm), _p(offsets), _p(counts),
                                                _p(slot_of_expert), n_slots, _p(slot_pool), slot_stride, WDT[wdt],
                                                _p(shared_w), _p(y_perm), _y_code(y_perm), _p(status), _s(stream)))
@@ -200,29 +229,6 @@ def _rows(name, t, shape, dtype) -> int:
 def _dense(name, t, shape, dtype) -> None:
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-
-
-def _expert_tensors(T, d, f, E, k, wdt, perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
-                    y_perm) -> None:
-    """Checks that the kernels of a grouped expert call stay inside its tensors (the library has their addresses alone)."""
-    i32 = _torch().int32
-    if not (perm.dtype == offsets.dtype == counts.dtype == slot_of_expert.dtype == i32 and perm.numel() >= T * k
-            and offsets.numel() > E and slot_of_expert.numel() >= E):
-        for name, t, n in (("perm", perm, T * k), ("offsets", offsets, E + 1), ("counts", counts, E),
-                           ("slot_of_expert", slot_of_expert, E)):
-            if t.dtype != i32 or t.numel() < n:
-                raise ValueError(f"{name} must be int32 of {n} elements at least, got {t.dtype} {list(t.shape)}")
-    _contig(perm, offsets, counts, slot_of_expert, y_perm, slot_pool, shared_w)
-    _y_code(y_perm)
-    rows, slot = T * k, slot_bytes(d, f, wdt)
-    if shared_w is not None:
-        rows += T
-        if shared_w.nbytes < slot:
-            raise ValueError(f"shared_w must hold {slot} bytes, got {shared_w.nbytes}")
-    if y_perm.numel() < rows * d:
-        raise ValueError(f"y_perm must hold {rows} rows of {d}, got {list(y_perm.shape)}")
-    if slot_pool.nbytes < (n_slots - 1) * slot_stride + slot:
-        raise ValueError(f"slot_pool must hold {n_slots} slots of {slot_stride} bytes, got {slot_pool.nbytes} bytes")
 
 
 def _quantised_out(x, shape, q, scale):

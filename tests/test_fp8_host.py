@@ -264,3 +264,21 @@ def test_expert_tensors_that_the_kernels_would_pass_the_end_of(moe):
         moe.expert_ffn_fp8(x, xs, **dict(good, y_perm=good["y_perm"].half()))
     with pytest.raises(ValueError, match="contiguous"):
         moe.expert_ffn_fp8(x, xs, **dict(good, slot_pool=torch.zeros(2, 2 * good["slot_pool"].numel(), dtype=torch.uint8)[:, ::2]))
+
+
+@pytest.mark.parametrize("wdt", ["bf16", "int4", "fp8"])
+def test_grouped_tensors_that_the_kernels_would_pass_the_end_of(moe, wdt):
+    """The same of the calls with bf16 rows (only calls that are refused: nothing is launched)."""
+    import torch
+
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    good = _grouped_tensors(moe, wdt)
+    for name, t in _wrong_sizes(good):
+        bad = dict(good, **{name: t})
+        with pytest.raises(ValueError, match=name):
+            moe.expert_ffn_grouped(x, wdt=wdt, **bad)
+        with pytest.raises(ValueError, match=name):
+            moe.expert_ffn_grouped_noalloc(x, wdt=wdt, **bad)
+    for status in (torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int16)):
+        with pytest.raises(ValueError, match="status"):
+            moe.expert_ffn_grouped_noalloc(x, wdt=wdt, status=status, **good)
