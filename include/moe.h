@@ -258,8 +258,9 @@ MOE_API moe_status moe_combine(const void* y_perm, moe_dtype y_dtype, const floa
  *   (both or neither), quantised from y before its rounding to act; at least one of y and q.
  *   weight [d] act or F32 (w_dtype).  ldx, ldr, ldro, ldy, ldq: elements from a row to the next,
  *   at least d (ignored for NULL pointers).
- * Rows: each is read once; one whose h^2 overflow binary32 gives zeros, one with a NaN or an infinity
- * NaN.  The result of a row does not depend on T.  resid_out may be x or residual, y may be x or
+ * Rows: each is read once.  One with a NaN is NaN throughout.  Where h^2 or their sum pass binary32's
+ * range the mean is infinite: finite columns give zeros, infinite ones NaN (in 8 bits: their groups of
+ * 128 read back as NaN, the others as zeros).  The result of a row does not depend on T.  resid_out may be x or residual, y may be x or
  * residual (same stride); no other overlap.  Any d from 1 to 16384 and any alignment to the
  * element; rows on 16 bytes (q on 8) with d a multiple of 8 are faster. */
 MOE_API moe_status moe_add_rmsnorm(const void* x, moe_dtype act, int T, int d, size_t ldx, const void* residual,

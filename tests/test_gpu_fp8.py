@@ -180,6 +180,29 @@ def test_norm_in_place_and_row_independence(moe):
     assert np.array_equal(_bits(x2), _bits(y)) and np.array_equal(_bits(r2), _bits(h))
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_norm_of_infinities_and_overflow(moe, act):
+    """An infinite mean: finite columns give zeros, infinite ones NaN, in 8 bits their groups; a NaN takes its row."""
+    import torch
+
+    T, d = 6, 400  # the last group has 16 columns
+    x = _rows(np.random.default_rng(1), T, d, torch.float32)
+    x[0, 5], x[1, 130], x[1, 399], x[2] = float("inf"), -float("inf"), float("inf"), 3e38
+    x[3, 7], x[4, 9], x[4, 300] = 1e25, float("nan"), float("inf")
+    x = x.to(torch.bfloat16 if act == "bf16" else torch.float32)
+    w = torch.ones(d, dtype=x.dtype, device="cuda")
+    y, _, q, s = moe.add_rmsnorm(x, w, emit="both")
+    v = fp8.rows_value(fp8.decode(_bits(q)), s.cpu().numpy().astype(np.float64))
+    y = y.double().cpu().numpy()
+    columns, groups = {0: [5], 1: [130, 399], 2: [], 3: [], 4: range(d)}, {0: [0], 1: [1, 3], 2: [], 3: [], 4: range(4)}
+    for t in range(5):
+        nan = np.isin(np.arange(d), list(columns[t]))
+        assert np.isnan(y[t][nan]).all() and not y[t][~nan].any()
+        nan = np.isin(np.arange(d) // 128, list(groups[t]))
+        assert np.isnan(v[t][nan]).all() and not v[t][~nan].any()
+    _check_norm(x[5:], None, w, 1e-6, torch.from_numpy(y[5:]).to(x.dtype), None, q[5:], s[5:])
+
+
 # ---- the dense product ------------------------------------------------------------------------------
 def _operands(rng, M, N, K, lda=None, ldw=None):
     """Quantised operands; columns past K of a wider row hold NaN codes."""
