@@ -3,7 +3,7 @@
 Builds every source of libmoe with AddressSanitizer and UndefinedBehaviorSanitizer on the host
 pass only (device code is compiled as usual), links it to _build/asan/libmoe.so, and runs the
 CPU tests that drive the host code through the C ABI -- the slot cache and its policy mode, the
-host expert with its thread pool, argument validation of every entry point -- against that build
+host expert with its thread pool, the packing of fp8 slots, argument validation of every entry point -- against that build
 (MOE_LIB_PATH), with the sanitizer runtime preloaded into Python.  Any report ends the run with a
 non-zero status.
 
@@ -27,7 +27,7 @@ from expert_offload_cache_amd import build as b  # noqa: E402
 
 OUT_DIR = os.path.join(ROOT, "_build", "asan")
 LIB = os.path.join(OUT_DIR, "libmoe.so")
-TESTS = ["tests/test_cache_host.py", "tests/test_cpu_expert.py", "tests/test_abi.py"]
+TESTS = ["tests/test_cache_host.py", "tests/test_cpu_expert.py", "tests/test_abi.py", "tests/test_fp8_host.py"]
 # host-pass only: every sanitizer flag goes through -Xarch_host
 HOST_SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer",
