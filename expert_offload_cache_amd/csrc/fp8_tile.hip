@@ -25,6 +25,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <string>
 #include <type_traits>
 
 #include "ffn_common.h"
@@ -430,9 +431,12 @@ moe_status launch_gemm(const GemmFp8& g, hipStream_t st) {
     const int lds = TL::gemm_lds(g.G);
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     const dim3 grid((unsigned)blocks_of(g.N, TL::kMT), (unsigned)blocks_of(g.M, TL::kNT));
-    ProfScope p("gemm_fp8_tile", st);
+    // weight rows x tokens x groups of waves, steps that the weights are ahead: a profile tells the tiles apart
+    static const std::string name = "gemm_fp8_tile_" + std::to_string(TL::kMT) + "x" + std::to_string(TL::kNT) + "x" +
+                                    std::to_string(KG) + "_" + std::to_string(RW);
+    ProfScope p(name.c_str(), st);
     kern<<<grid, NW * KG * 64, lds, st>>>(g);
-    return check_launch("gemm_fp8_tile");
+    return check_launch(name.c_str());
 }
 
 // ---- the routed experts' projections ------------------------------------------------------------------

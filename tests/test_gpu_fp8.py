@@ -301,6 +301,62 @@ def test_bf16_product_of_outliers_and_small_values(moe, M, N, K):
     assert (np.abs(y_to_f64(moe.gemm_fp8(*dev, out_dtype=torch.float32)[at]) - ref) <= sums).all()
 
 
+# weight rows x tokens x groups of waves, steps ahead -> shapes whose steps are whole (K a multiple of 128, and of 256
+# where two groups share them) and shapes whose last step ends early or does not exist for the second group
+TILES = {
+    "bf16": {"512x128x1_1": [(1500, 8200, 1024), (1500, 8200, 1040)], "256x128x1_2": [(4000, 2000, 1024), (4000, 2000, 1040)],
+             "256x64x1_2": [(200, 8200, 1152), (200, 8200, 1040)], "128x64x1_2": [(100, 8200, 1152), (100, 8200, 1040)],
+             "64x64x1_2": [(100, 257, 384), (100, 257, 272)], "128x64x2_2": [(100, 8200, 1024), (100, 8200, 1168)],
+             "64x64x2_2": [(300, 257, 1280), (300, 257, 1040)], "64x64x2_1": [(200, 8200, 1024), (200, 8200, 1168)]},
+    "f32": {"256x128x1_1": [(2050, 2000, 1024), (2050, 2000, 1040)], "128x64x1_3": [(100, 8200, 1024), (100, 8200, 1040)],
+            "64x64x1_3": [(200, 8200, 1024), (200, 8200, 1040)], "64x64x2_2": [(513, 257, 1280), (513, 257, 1040)]}}
+
+
+@pytest.mark.parametrize("out,tile,shape", [(o, t, s) for o in TILES for t in TILES[o] for s in TILES[o][t]])
+def test_product_in_every_tile(moe, out, tile, shape):
+    """Each tile, by the name that it has in a profile, with whole steps and without; a NaN of a row or a matrix row
+    and an infinite scale reach that row or column alone.
+
+    bf16 results: besides the result's rounding (2^-8) and the terms' ((K + 4 G) u M) a run of 8 inputs is cut by less
+    than 2^-10 of its largest product (fp8.h; the few subnormals here are no run's largest), so an element by 2^-10 M.
+    Over a matrix these cuts, independent of each other, add up as their squares: K / 8 of them, each of a largest
+    product of some 4 deviations, against the sum of K products of one: 2^-10 * 4 / sqrt(8) = 2^-9.5 of its norm."""
+    import torch
+
+    M, N, K = shape
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    ops, (a, sa, w, sw) = _operands(np.random.default_rng([M, N, K]), M, N, K)
+    moe.profile_reset()
+    moe.profile_enable(True)
+    try:
+        c = moe.gemm_fp8(a, sa, w, sw, out_dtype=dt)
+        torch.cuda.synchronize()
+        moe.profile_collect()
+        names = set(moe.profile_results())
+    finally:
+        moe.profile_enable(False)
+        moe.profile_reset()
+    assert names == {"gemm_fp8_tile_" + tile}
+    if out == "f32":
+        _check_product(ops, c, fast=False)
+    else:
+        A, W = fp8.rows_value(fp8.decode(ops[0]), ops[1].astype(np.float64)), fp8.matrix_value(ops[2], ops[3])
+        ref, mag = A @ W.T, np.abs(A) @ np.abs(W).T
+        err = np.abs(y_to_f64(c) - ref)
+        assert (err <= (2.0 ** -10 + (K + 4 * ops[1].shape[1]) * U) * (1 + 2.0 ** -8) * mag + 2.0 ** -8 * np.abs(ref)).all()
+        assert np.linalg.norm(err) <= (2.0 ** -8 + 2.0 ** -9.5) * np.linalg.norm(ref)
+    sa[M - 3, -1], sa[5, 0] = float("inf"), float("inf")
+    for t, r, k, code in ((w, 7, 100, 0x7F), (w, N - 1, K - 1, 0xFF), (a, 9, K - 1, 0x7F), (a, M - 1, 0, 0xFF)):
+        t.view(torch.uint8)[r, k] = code
+    d = moe.gemm_fp8(a, sa, w, sw, out_dtype=dt)
+    rows, cols = torch.ones(M, dtype=torch.bool, device="cuda"), torch.ones(N, dtype=torch.bool, device="cuda")
+    rows[[9, M - 1, 5, M - 3]] = False
+    cols[[7, N - 1]] = False
+    assert torch.isnan(d[[9, M - 1]]).all() and torch.isnan(d[:, ~cols]).all()
+    assert not torch.isfinite(d[[5, M - 3]]).any()
+    assert torch.equal(d[rows][:, cols], c[rows][:, cols])
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 150, 700])
 def test_product_strides(moe, M):
     """Wider rows (their rest NaN), a result inside a wider matrix at an odd element, and nothing written
