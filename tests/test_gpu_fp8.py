@@ -625,6 +625,151 @@ def test_expert_chosen_twice_and_shared_slots(moe, T):
     assert torch.equal(alone["y_perm"][alone["inv_perm"].long()].view(T, 3, -1)[:, 0], rows[:, 0])
 
 
+def _down_tiles(counts, T, shared, d):
+    """What the launch of a down projection into bf16 rows chooses from the counts (fp8_tile.hip): the rows of its
+    128-token tiles (None: all experts take 256 x 64), and the 64-token chunks that 256 x 64 tiles take beside them."""
+    n = list(counts) + ([T] if shared else [])
+    chunks = lambda nt, lo, hi: sum(-(-v // nt) for v in n if lo <= v <= hi)
+    tiles = lambda c, rows: c * -(-d // rows)
+    if tiles(chunks(64, 0, 1 << 30), 256) <= 256:
+        return None, chunks(64, 0, 1 << 30)
+    heavy = chunks(128, 65, 1 << 30)
+    rounds = lambda rows: -(-tiles(heavy, rows) // 256)
+    return 512 if rounds(512) * 2.1 < rounds(256) * 1.27 else 256, chunks(64, 0, 64)
+
+
+# (layer, tokens of each expert, rows of the tiles that the heavy ones take in the down projection)
+MIXED = [(dict(d=4096, f=128, E=8), [900, 300, 65, 64, 1, 30, 0, 17], 256),
+         (dict(d=4096, f=128, E=8, shared=True), [20, 1, 700, 129, 0, 63, 66, 128], 512),
+         (dict(d=8192, f=256, E=6), [1500, 64, 0, 5, 640, 33], 256),
+         (dict(d=8192, f=256, E=6), [1400, 64, 0, 5, 640, 33], 512),
+         # more experts than the table in LDS holds
+         (dict(d=8192, f=128, E=300), {0: 700, 63: 64, 64: 900, 70: 3, 255: 250, 256: 130, 299: 40, 298: 1}, 256),
+         (dict(d=8192, f=128, E=300), {0: 640, 63: 64, 64: 900, 70: 3, 255: 250, 256: 128, 299: 40, 298: 1}, 512)]
+
+
+def _mixed_call(moe, layer, li, counts, k=1):
+    """Route tokens so that expert e gets counts[e] of them -> (x, expert of each token, the sort's outputs)."""
+    ids = np.repeat(np.arange(len(counts)), counts).astype(np.int32)
+    np.random.default_rng(3).shuffle(ids)
+    x = layer.x_to_device(li.x)
+    return x, ids, moe.route_permute(x, layer.w_router, layer.bias, k, forced_idx=to_dev(ids[:, None], "i32"))
+
+
+@pytest.mark.parametrize("shape,counts,rows", MIXED, ids=[f"{m[0]['d']}x{m[0]['f']}x{m[0]['E']}" + ("s" if "shared" in m[0] else "") + f"_{m[2]}"
+                                                          for m in MIXED])
+def test_heavy_and_light_experts_in_one_call(moe, shape, counts, rows):
+    """Experts above and below 64 tokens in one launch: an expert's rows have the bits of a call with that expert alone
+    (the order of the sums does not depend on the tile), and the layer's output is the oracle's."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    if isinstance(counts, dict):
+        counts = [counts.get(e, 0) for e in range(shape["E"])]
+    T, E, d, f, shared = sum(counts), shape["E"], shape["d"], shape["f"], shape.get("shared", False)
+    heavy, light = _down_tiles(counts, T, shared, d)
+    assert heavy == rows and light > 0
+    wl = small_workload("bf16", "fp8", d, f, E, 1, shared=shared)
+    li = synth.layer_inputs(wl, T, seed=1, with_experts=False)
+    used = {e: synth.expert_weights(wl, 1, 0, e) for e in range(E) if counts[e] or e == 0}
+    li.experts = [used.get(e, used[0]) for e in range(E)]
+    li.shared = synth.expert_weights(wl, 1, 0, 0, shared=True) if shared else None
+    layer = DeviceLayer.from_inputs(li)
+    x, ids, (_, tw, _, cnt, off, perm, inv) = _mixed_call(moe, layer, li, counts)
+    assert cnt.tolist() == counts
+    args = (layer.pool, layer.n_slots, layer.stride, "fp8", f, 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bounds = off.tolist()
+    for dt in (torch.bfloat16, torch.float32):
+        y, ws = moe.expert_ffn_grouped(x, perm, off, cnt, layer.slot_of_expert, *args, shared_w=layer.shared, y_dtype=dt)
+        assert int(ws[:4].view(torch.int32).item()) == 0
+        for e in [e for e in range(E) if counts[e] > 16]:  # up to 16 tokens alone are streamed
+            lo, hi = bounds[e], bounds[e + 1]
+            alone, _ = moe.expert_ffn_grouped(x[perm[lo:hi].long()].contiguous(), torch.arange(hi - lo, **i32),
+                                              torch.tensor([0, hi - lo], **i32), torch.tensor([hi - lo], **i32),
+                                              layer.slot_of_expert[e:e + 1].contiguous(), *args, y_dtype=dt)
+            assert np.array_equal(_bits(alone), _bits(y[lo:hi])), e
+        got = moe.combine(y, tw, inv, 1, shared, torch.bfloat16)
+        ref = moe_layer(li.x, li.w_router, li.bias, "bf16", 1, E, li.experts, li.shared, forced_idx=ids[:, None])
+        err = rel_err_per_token(y_to_f64(got), ref["y"])
+        assert err.max() <= 0.125 and err.mean() <= 5e-3, (err.max(), err.mean())
+
+
+def test_absent_and_elsewhere_slots_in_heavy_and_light_tiles(moe):
+    """An absent and a MOE_SLOT_ELSEWHERE expert on either side of 64 tokens: flagged and zeroed, left, the others' bits kept."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    counts, d, f = [700, 300, 200, 64, 40, 33, 129, 20], 4096, 256
+    assert _down_tiles(counts, sum(counts), False, d) == (256, 4)
+    wl = small_workload("bf16", "fp8", d, f, 8, 1)
+    li = synth.layer_inputs(wl, sum(counts), seed=2)
+    layer = DeviceLayer.from_inputs(li)
+    x, _, (_, _, _, cnt, off, perm, _) = _mixed_call(moe, layer, li, counts)
+    soe = layer.slot_of_expert.clone()
+    soe[0], soe[4], soe[2], soe[5] = -1, layer.n_slots, -2, -2
+    bounds = off.tolist()
+    for dt in (torch.bfloat16, torch.float32):
+        args = (layer.pool, layer.n_slots, layer.stride, "fp8", f, 1)
+        ref, ws = moe.expert_ffn_grouped(x, perm, off, cnt, layer.slot_of_expert, *args, y_dtype=dt)
+        assert int(ws[:4].view(torch.int32).item()) == 0
+        y, ws = moe.expert_ffn_grouped(x, perm, off, cnt, soe, *args, y_perm=torch.full_like(ref, 123.0))
+        assert int(ws[:4].view(torch.int32).item()) == 1
+        for e in range(8):
+            got, want = y[bounds[e]:bounds[e + 1]], ref[bounds[e]:bounds[e + 1]]
+            assert not got.any() if e in (0, 4) else (got == 123.0).all() if e in (2, 5) else torch.equal(got, want)
+
+
+@pytest.mark.parametrize("y", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_nan_and_infinity_through_the_experts(moe, T, y):
+    """A NaN or an infinity of a token makes its rows NaN, of a down row its expert's column, of an expert's gate row or
+    an infinite weight scale that expert's rows or columns; every other value keeps its bits."""
+    import torch
+    from expert_offload_cache_amd.layer import DeviceLayer
+
+    d, f, E, dt = 384, 256, 4, torch.bfloat16 if y == "bf16" else torch.float32
+    wl = small_workload("bf16", "fp8", d, f, E, 2, shared=True)
+    li = synth.layer_inputs(wl, T, seed=4)
+    forced = np.stack([np.random.default_rng(t).permutation(E)[:2] for t in range(T)]).astype(np.int32)
+    layer = DeviceLayer.from_inputs(li)
+    x = layer.x_to_device(li.x)
+    _, _, _, cnt, off, perm, _ = moe.route_permute(x, layer.w_router, layer.bias, 2, forced_idx=to_dev(forced, "i32"))
+
+    def call(x, pool):
+        return moe.expert_ffn_grouped(x, perm, off, cnt, layer.slot_of_expert, pool, layer.n_slots, layer.stride, "fp8", f, 2,
+                                      shared_w=layer.shared, y_dtype=dt)[0]
+
+    ref = call(x, layer.pool)
+    x2 = x.clone()
+    x2[0, 5], x2[T - 1, 300] = float("nan"), -float("inf")
+    hit = torch.cat([torch.isin(perm // 2, torch.tensor([0, T - 1], device="cuda")),
+                     torch.isin(torch.arange(T, device="cuda"), torch.tensor([0, T - 1], device="cuda"))])
+    got = call(x2, layer.pool)
+    assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], ref[~hit])
+
+    # expert 1: a NaN in row 77 of its down matrix; 2: one in its gate matrix; 3: an infinite scale of a down block
+    pool = layer.pool.clone().view(-1)
+    at = {e: int(layer.slot_of_expert[e]) * layer.stride for e in range(E)}
+    gu, dn = 16 * d + 64, 16 * f + 64
+    down = 2 * (f // 16) * gu
+    pool[at[1] + down + (77 // 16) * dn + 16 * (77 % 16)] = 0x7F  # lane 77 % 16 of the first fragment: input 0
+    pool[at[2] + 2 * gu] = 0xFF
+    inf = torch.tensor([float("inf")], device="cuda").view(torch.uint8)
+    for block in range(8, 16):  # rows 128 .. 255, inputs 128 .. 255
+        o = at[3] + down + block * dn + 16 * f + 4
+        pool[o:o + 4] = inf
+    got = call(x, pool.view_as(layer.pool))
+    b = off.tolist()
+    rows = [slice(b[e], b[e + 1]) for e in range(E)]
+    cols = torch.arange(d, device="cuda")
+    assert torch.isnan(got[rows[1]][:, 77]).all() and torch.equal(got[rows[1]][:, cols != 77], ref[rows[1]][:, cols != 77])
+    assert torch.isnan(got[rows[2]]).all()
+    block = (cols >= 128) & (cols < 256)
+    assert not torch.isfinite(got[rows[3]][:, block]).any() and torch.equal(got[rows[3]][:, ~block], ref[rows[3]][:, ~block])
+    assert torch.equal(got[rows[0]], ref[rows[0]]) and torch.equal(got[2 * T:], ref[2 * T:])
+
+
 def test_graphs_that_share_a_workspace(moe):
     """Two captured calls of different lengths take turns on the workspace of the longer one."""
     import torch
