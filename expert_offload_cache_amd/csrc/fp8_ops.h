@@ -56,8 +56,8 @@ struct FfnFp8 {
     uint8_t* h8 = nullptr;
     float* h_scale = nullptr;
 };
-// Up to 16 tokens a streamed call is one token block an expert.  16 tokens on 51 of 256 experts of 4096 x 2048 take
-// 231 us streamed, 17 on 52 250 us in tiles; where all choose the same 6 experts, which is rare, 81 and 38.
+// Up to 16 tokens a streamed call is one token block an expert.  16 tokens on 50 of 256 experts of 4096 x 2048 and the
+// shared one take 234 us streamed, 17 on 51 256 us in tiles; where all choose the same 6 experts, which is rare, 85 and 58.
 constexpr int kFp8Stream = 16;
 
 // bf16 rows [T, d], back to back, into e4m3 rows and scales (norm.hip)

@@ -15,9 +15,10 @@
 // four lanes l, l ^ 16, l ^ 32, l ^ 48 hold the 128 inputs of a token's group between them.
 //
 // Experts: one token on 6 of 256 experts of 4096 x 2048 and the shared one (176 MB) 25 + 13.5 us, 4.6 TB/s; 16 tokens
-// on 51 of them 231 us, 5.5 TB/s (with the tokens prepared again for each row block: 453).
-// Dense: one row against 4096 x 2048 (8.4 MB) 4.4 us, of which 3 are a launch and its first loads; 37 rows against
-// 2048 x 4096 9.6 us, bound by the chain of a wave's 4 steps (loads, widening, four products, four multiply-adds).
+// on 50 of them and the shared one 234 us, 5.5 TB/s (with the tokens prepared again for each row block: 453).
+// Dense: one row against 4096 x 2048 (8.4 MB) 4.3 us, of which 3 are a launch and its first loads; 37 rows against
+// 2048 x 4096 9.6 us, a wave's 4 steps one after the other: the 32 x 16 and 32 x 32 blocks hold one step in flight, so each
+// step's loads wait for the step before.  Deeper rings were measured for the 16 x 16 block alone.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -8,20 +8,22 @@
 // Both operands go through LDS by direct-to-LDS loads: the tokens, which every wave reads, in a ring of
 // RX steps; each wave's weight rows in a ring of RW steps of its own.  (Weights straight into
 // registers take two register sets, which does not leave room for the products in flight: experts of
-// 8192 tokens 1.69 ms against 1.61; and operand-order loads of a row-major matrix touch 16 rows at a
-// time.)  The scales of the whole tile are put into LDS once, before the first step.
+// 8192 tokens 1.69 ms against 1.61, both with e4m3 sums; and operand-order loads of a row-major matrix
+// touch 16 rows at a time.)  The scales of the whole tile are put into LDS once, before the first step.
 //
 // Gate/up: a wave's row blocks are gate and up blocks in turn, so SwiGLU happens in registers; the
 // 16 / RA waves that share a 128-column group of h join their largest magnitudes through LDS, and h is
 // written in 8 bits with its scale.
 //
-// Measured: 8192 x 4096 x 4096 in 131 us, 2.1 PFLOP/s; 8192 tokens on 6 of 256 experts of 4096 x 2048 and the shared
-// one, the six the same, 905 + 505 us, 2.05 PFLOP/s.  Counters of the first: the matrix cores are busy 56 % of the units'
-// cycles (2.0 GHz under this load), the vector units about as much (four multiply-adds a product and one instruction
-// more), LDS 28 %, bank conflicts 3 % of that; the loop holds 32 products in 285 instructions.  What is left is two
-// waves a SIMD that both wait at a step's barrier and for operands one block ahead: the accumulators, 128 registers,
-// leave no room for a third wave or a longer lead (reading two token blocks ahead, 32 x 32 products and buffer
-// loads to LDS gained nothing).
+// Measured: 8192 x 4096 x 4096 in 125 to 131 us, 2.1 to 2.2 PFLOP/s.  Counters: the matrix cores are busy 60 % of the
+// units' cycles, the vector units about as much (four multiply-adds a product and one instruction more), LDS 29 %, bank
+// conflicts 3 % of that; the loop holds 32 products in 285 instructions.  What is left is two waves a SIMD that both wait
+// at a step's barrier and for operands one block ahead: the accumulators, 128 registers, leave no room for a third
+// wave or a longer lead (reading two token blocks ahead, 32 x 32 products and buffer loads to LDS gained nothing).
+// 8192 tokens on 6 of 256 experts of 4096 x 2048 and the shared one, the six the same: gate/up 1750 to 1890 us,
+// 1.0 to 1.1 PFLOP/s (the library's bf16 product of 8192^3 reaches 1.63), the bf16 rows of the down projection 490 to 505,
+// 1.9 PFLOP/s.  Gate/up: the matrix cores 50 % busy, LDS 16 %; four vector instructions beside each matrix instruction,
+// two of them widenings, since every wave widens the tokens' operands for itself.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -520,8 +522,8 @@ __device__ __forceinline__ void find_in_table(const FfnArgs& a, const Table& tb,
 
 // This workgroup's tiles of the experts that hold n_lo to n_hi tokens (chunks: their chunks of kNT).  Workgroup
 // i runs on XCD i mod 8; each XCD takes a run of consecutive tiles, so that the tiles that read the same
-// weights or the same tokens share an L2 (2048 tokens, 8 of 128 experts of 2048 x 768: 254 -> 236 us against tiles
-// dealt out in turn, 8192 on 7 of 4096 x 2048: 1597 -> 1526).
+// weights or the same tokens share an L2 (both projections with e4m3 sums, 2048 tokens, 8 of 128 experts of 2048 x 768:
+// 254 -> 236 us against tiles dealt out in turn, 8192 on 7 of 4096 x 2048: 1597 -> 1526).
 template <int MODE, bool EXACT, int RA, int NTB, int NW, int RW, int RX>
 __device__ __forceinline__ void ffn_tiles(Tile8<RA, NTB, NW, RW, RX>, const FfnFp8& p, const Table& tb, uint8_t* smem, int n_lo, int n_hi, int chunks, int first) {
     using TL = Tile8<RA, NTB, NW, RW, RX>;
@@ -659,16 +661,19 @@ __device__ __forceinline__ void ffn_tiles(Tile8<RA, NTB, NW, RW, RX>, const FfnF
 // So are the down projection's where its rows are binary32; bf16 rows take the e4m3 instruction, as the dense product.
 //
 // EXACT: 512 x 64 or 256 x 64, whichever needs the less time for its rounds over the compute units at a cost of 7 to
-// 4.  Measured (us of the gate/up projection, 512 x 64 / 256 x 64 / 256 x 128): 64 tokens on each of 8 experts of
-// 2048 x 768 34 / 25 / 36, 517 38 / 47 / 40; 4096 x 2048, 128 on each of 7 60 / 44 / 63, 8192 1712 / 2162 / 1770;
-// popularity as 1 / rank^1.1, 6 of 256 of 4096 x 2048 and the shared one, 64 tokens 338 / 367 / 573, 2048 997 / 1164 /
-// 1442, 8192 2196 / 2713 / 2631.  (512 x 128 does not fit the registers: 64 of them hold the weights as bf16.)
+// 4.  Measured (us of the gate/up projection, before its exact quotient, which adds 1 to 2 us a tile; 512 x 64 / 256 x 64 /
+// 256 x 128): 64 tokens on each of 8 experts of 2048 x 768 34 / 25 / 36, 517 38 / 47 / 40; 4096 x 2048, 128 on each of 7
+// 60 / 44 / 63, 8192 1712 / 2162 / 1770; popularity as 1 / rank^1.1, 6 of 256 of 4096 x 2048 and the shared one, 64
+// tokens 338 / 367 / 573, 2048 997 / 1164 / 1442, 8192 2196 / 2713 / 2631.  (512 x 128 does not fit the registers: 64 of
+// them hold the weights as bf16.)
 //
 // Else (bf16 rows of the down projection):
 // - All experts 256 rows x 64 tokens where each such tile has a compute unit of its own.
 // - Else experts with up to kLight tokens take 256 x 64, with the weights two steps ahead (their weights' bytes
 //   bound them), and the others 512 x 128 or 256 x 128, whichever needs the less time for its rounds over the
-//   compute units at 2.1 and 1.27 us a step (the dense product's costs).
+//   compute units at 2.1 and 1.27 us a step (the dense product's costs).  Measured (us, 512 x 128 / 256 x 128 /
+//   256 x 64 alone): 128 tokens on each of 7 experts of 4096 x 2048 30 / 22 / 22, 517 62 / 64 / 64, 4096 251 / 313 / 422;
+//   8192 by popularity on 6 of 256 725 / 887 / 1080 (750 as chosen), on 8 of 128 of 2048 x 768 178 / 226 / 289 (183).
 // HEAVY false: no expert of the call can hold more than kLight, or the larger tiles' scales exceed the LDS
 // (inputs beyond 10752).
 constexpr int kLight = 64, kMost = 1 << 30, kWaves = 8;
@@ -756,6 +761,7 @@ constexpr TileCost kTiles[] = {
     cost<2, 4, 8, 2, 4, 1, false>(0.66f, 0.77f), cost<2, 4, 4, 2, 4, 1, false>(0.49f, 0.40f),
     cost<1, 4, 4, 2, 4, 1, false>(0.39f, 0.27f), cost<2, 4, 4, 2, 4, 2, false>(0.82f, 0.90f),
     cost<1, 4, 4, 2, 4, 2, false>(0.57f, 0.65f), cost<1, 4, 4, 1, 3, 2, false>(0.68f, 0.50f)};
+// (binary32 results of 8192 x 4096 x 4096 278 to 325 us: every wave widens every token block of its tile for itself)
 constexpr TileCost kExactTiles[] = {
     cost<2, 8, 8, 1, 4, 1, true>(1.70f, 2.10f), cost<2, 4, 4, 3, 5, 1, true>(0.72f, 0.78f),
     cost<1, 4, 4, 3, 5, 1, true>(0.61f, 0.45f), cost<1, 4, 4, 2, 4, 2, true>(0.88f, 0.95f)};

@@ -12,7 +12,7 @@
 // the width alone, so a row's bits do not depend on how many rows the call has.
 //
 // Bound by memory: 8192 bf16 rows of 4096 with a residual and both outputs (303 MB) 58 us, 5.2 TB/s;
-// 8192 bf16 rows of 2048 quantised (51 MB) 9.6 us, 5.3 TB/s (a 4 GiB copy reaches 4.8 TB/s; some of
+// 8192 bf16 rows of 2048 quantised (51 MB) 9.5 us, 5.3 TB/s (a 4 GiB copy reaches 4.8 TB/s; some of
 // these rows are still in the last-level cache).  At most 16 columns a lane, so that a row stays in registers
 // (28 of them at 4096 columns) and a compute unit holds 8 waves a SIMD.  One row of 4096 takes 4 us, a launch.
 #include <hip/hip_runtime.h>

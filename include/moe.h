@@ -192,8 +192,9 @@ MOE_API moe_status moe_route_permute(const void* x, moe_dtype act, int T, int d,
  * are of 8-bit values again: bitwise what moe_quant_fp8 and moe_expert_ffn_fp8 give.  Sums are
  * binary32, but for the down projection of calls above 16 tokens into BF16 rows, which are summed as
  * the BF16 results of moe_gemm_fp8.  The order of the sums differs between calls of up to 16 tokens and
- * longer ones: an element of h that lies on a border between two e4m3 values to within it may take the
- * other one, which moves a token's row by some 2e-4 of its norm. */
+ * longer ones, so a token's row does: F32 rows by some 2e-7 of their norm (BF16 rows by 3e-4, the roundings
+ * that fall otherwise), and by up to some 1e-3 where an element of h lies so near to a border between two
+ * e4m3 values that it takes the other one. */
 #define MOE_SLOT_ELSEWHERE (-2)
 /* Above 64 tokens (prefill) the experts run on the matrix-core grouped GEMM, which feeds int4
  * weights to the matrix cores as bf16(q * s).  Experts holding at most moe_prefill_gemv_tokens(w)
