@@ -540,7 +540,8 @@ CANCEL, CANCEL_TOL = 24.0, 0.012
 
 
 @pytest.mark.parametrize("y", ["f32", "bf16"])
-@pytest.mark.parametrize("d,f,T", [(128, 128, 16), (128, 128, 17), (256, 128, 130), (128, 16384, 200)])
+@pytest.mark.parametrize("d,f,T", [(128, 128, 16), (128, 128, 17), (256, 128, 130), (128, 16384, 200), (16384, 128, 70),
+                                   (16384, 1024, 2200)])
 def test_gate_and_up_sums_are_binary32(moe, d, f, T, y):
     """Two large products that cancel leave the small ones beside them, streamed and in either tile.
 
