@@ -14,7 +14,7 @@ import numpy as np
 from ._lib import (MOE_BF16, MOE_F32, MOE_FP8_B128, MOE_INT4_G128, MoeError, check, lib)
 
 __all__ = ["route", "permute", "permute_workspace", "permute_workspace_bytes", "route_permute", "expert_ffn_grouped", "expert_ffn_grouped_noalloc", "expert_ffn_fp8", "combine",
-           "add_rmsnorm", "quant_fp8", "gemm_fp8",
+           "layer_few", "layer_few_workspace_bytes", "add_rmsnorm", "quant_fp8", "gemm_fp8",
            "slot_bytes", "pack_expert", "workspace_bytes", "hybrid_split", "SlotCache", "pinned_alloc", "pinned_free", "profile_enable",
            "profile_collect", "profile_results", "profile_reset", "MoeError", "WDT", "lib"]
 
@@ -352,6 +352,51 @@ def combine(y_perm, topk_w, inv_perm, k: int, has_shared: bool, out_dtype, y=Non
     check(lib().moe_combine(_p(y_perm), _y_code(y_perm), _p(topk_w), _p(inv_perm), T, k, d, int(bool(has_shared)),
                             _p(y), code, _s(stream)))
     return y
+
+
+def layer_few_workspace_bytes(T: int, d: int, f: int, E: int, k: int, has_shared: bool, wdt: str) -> int:
+    return int(lib().moe_layer_few_workspace_bytes(T, d, f, E, k, int(bool(has_shared)), WDT[wdt]))
+
+
+def layer_few(x, w_router, bias, k: int, slot_of_expert, slot_pool, n_slots: int, slot_stride: int, wdt: str, f: int,
+              shared_w=None, forced_idx=None, out=None, ws=None, stream=None):
+    """The whole layer for at most 16 tokens (moe_layer_few): route, experts and combine in two launches.
+    x [T, d], w_router [E, d] of x's type; bias f32 [E] or None; slots as expert_ffn_grouped takes them.
+    out: (y, topk_idx, topk_w) to write into; ws: layer_few_workspace_bytes, zero-filled before its first use
+    and used by one call at a time.  -> (y [T, d], topk_idx int32 [T, k], topk_w f32 [T, k])."""
+    torch = _torch()
+    act = _act(x)
+    T, d = x.shape
+    E = w_router.shape[0]
+    dt, f32, i32 = x.dtype, torch.float32, torch.int32
+    if out is None:
+        out = (torch.empty((T, d), dtype=dt, device=x.device), torch.empty((T, k), dtype=i32, device=x.device),
+               torch.empty((T, k), dtype=f32, device=x.device))
+    y, idx, w = out
+    for name, t, shape, dtype in (("x", x, (T, d), dt), ("w_router", w_router, (E, d), dt), ("y", y, (T, d), dt),
+                                  ("topk_idx", idx, (T, k), i32), ("topk_w", w, (T, k), f32)):
+        _dense(name, t, shape, dtype)
+    if bias is not None:
+        _dense("bias", bias, (E,), f32)
+    if forced_idx is not None:
+        _dense("forced_idx", forced_idx, (T, k), i32)
+    if slot_of_expert.dtype != i32 or slot_of_expert.numel() < E:
+        raise ValueError(f"slot_of_expert must be int32 of {E} elements at least, got {slot_of_expert.dtype} "
+                         f"{list(slot_of_expert.shape)}")
+    _contig(slot_of_expert, slot_pool, shared_w, ws)
+    slot = slot_bytes(d, f, wdt)
+    if shared_w is not None and shared_w.nbytes < slot:
+        raise ValueError(f"shared_w must hold {slot} bytes, got {shared_w.nbytes}")
+    if slot_pool.nbytes < (n_slots - 1) * slot_stride + slot:
+        raise ValueError(f"slot_pool must hold {n_slots} slots of {slot_stride} bytes, got {slot_pool.nbytes} bytes")
+    if ws is None:
+        ws = torch.zeros(layer_few_workspace_bytes(T, d, f, E, k, shared_w is not None, wdt) or 1, dtype=torch.uint8,
+                         device=x.device)
+    _on_current_device(x, w_router, bias, forced_idx, slot_of_expert, slot_pool, shared_w, y, idx, w, ws)
+    check(lib().moe_layer_few(_p(x), act, T, d, f, E, k, _p(w_router), _p(bias), _p(forced_idx), _p(slot_of_expert),
+                              n_slots, _p(slot_pool), slot_stride, WDT[wdt], _p(shared_w), _p(idx), _p(w), _p(y),
+                              _p(ws), ws.nbytes, _s(stream)))
+    return out
 
 
 # ---------------------------------------------------------------------------------------------

@@ -32,6 +32,8 @@ SIGNATURES = {
                                              _vp, _sz, _i32, _vp, _vp, _i32, _vp, _vp]),
     "moe_expert_ffn_fp8": (_st, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp, _vp,
                                  _i32, _vp, _sz, _vp]),
+    "moe_layer_few_workspace_bytes": (_sz, [_i32] * 7),
+    "moe_layer_few": (_st, [_vp] + [_i32] * 6 + [_vp] * 4 + [_i32, _vp, _sz, _i32] + [_vp] * 5 + [_sz, _vp]),
     "moe_add_rmsnorm": (_st, [_vp, _i32, _i32, _i32, _sz, _vp, _sz, _vp, _i32, ctypes.c_float, _vp, _sz, _vp, _sz, _vp,
                               _sz, _vp, _vp]),
     "moe_quant_fp8": (_st, [_vp, _i32, _i32, _i32, _sz, _vp, _sz, _vp, _vp]),

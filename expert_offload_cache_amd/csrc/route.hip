@@ -23,30 +23,13 @@
 #include <hip/hip_runtime.h>
 
 #include "moe_common.h"
+#include "route_logit.h"
 #include "select_permute.h"
 
 #include <algorithm>
 
 namespace moe {
 namespace {
-
-// acc + a*b with two roundings (a*b exact for bf16 inputs, so a fused form gives the same bits)
-template <bool kBf16>
-__device__ __forceinline__ float madd(float acc, float a, float b) {
-    if constexpr (kBf16) {
-        return __builtin_fmaf(a, b, acc);
-    } else {
-#pragma clang fp contract(off)
-        float p = a * b;
-        return acc + p;
-    }
-}
-
-template <bool kBf16>
-__device__ __forceinline__ float load_elem(const void* base, size_t i) {
-    if constexpr (kBf16) return bf16_to_f32(((const uint16_t*)base)[i]);
-    else return ((const float*)base)[i];
-}
 
 // ---- prefill logits: LDS tiles, 64 tokens x 64 experts per block ------------------------------
 constexpr int kTT = 64;  // tokens per tile

@@ -8,8 +8,8 @@ from typing import Optional
 
 import numpy as np
 
-from . import (add_rmsnorm, combine, expert_ffn_fp8, expert_ffn_grouped, pack_expert, permute_workspace, route_permute,
-               slot_bytes, workspace_bytes, y_perm_dtype, WDT)
+from . import (add_rmsnorm, combine, expert_ffn_fp8, expert_ffn_grouped, layer_few, layer_few_workspace_bytes,
+               pack_expert, permute_workspace, route_permute, slot_bytes, workspace_bytes, y_perm_dtype, WDT)
 from ._lib import MOE_BF16, MOE_F32
 
 
@@ -106,6 +106,40 @@ class DeviceLayer:
             y_perm=torch.empty((rows, d), dtype=y_perm_dtype(act, T), device=dev),
             y=torch.empty((T, d), dtype=act, device=dev),
             ws=self.workspace(T), pws=permute_workspace(T, k, E, dev))
+
+    def buffers_few(self, T: int):
+        """Outputs and workspace of a T-token forward_few (at most 16), allocated once."""
+        import torch
+
+        act = torch.bfloat16 if self.act == "bf16" else torch.float32
+        dev = self.device
+        norm = {}
+        if self.norm_weight is not None:
+            norm["norm"] = tuple(torch.empty((T, self.d), dtype=act, device=dev) for _ in range(2)) + (None, None)
+        n = layer_few_workspace_bytes(T, self.d, self.f, self.E, self.k, self.shared is not None, self.wdt)
+        return dict(**norm, few=(torch.empty((T, self.d), dtype=act, device=dev),
+                                 torch.empty((T, self.k), dtype=torch.int32, device=dev),
+                                 torch.empty((T, self.k), dtype=torch.float32, device=dev)),
+                    ws=torch.zeros(max(n, 1), dtype=torch.uint8, device=dev))
+
+    def forward_few(self, x, forced_idx=None, stream=None, slot_of_expert=None, bufs=None, residual=None):
+        """forward for at most 16 tokens through layer_few: two launches instead of six, no intermediate
+        rows.  Returns a dict with y [T, d], topk_idx, topk_w and, as forward, x and residual.  With `bufs` (from
+        buffers_few(T)) the outputs are written there."""
+        b = bufs or {}
+        kept = None
+        if self.norm_weight is not None:
+            out = b.get("norm")
+            if out is not None and residual is None:
+                out = (out[0], None, None, None)
+            x, kept, _, _ = add_rmsnorm(x, self.norm_weight, self.norm_eps, residual=residual, out=out, stream=stream)
+        elif residual is not None:
+            raise ValueError("a residual needs a layer with a norm weight")
+        soe = self.slot_of_expert if slot_of_expert is None else slot_of_expert
+        y, idx, w = layer_few(x, self.w_router, self.bias, self.k, soe, self.pool, self.n_slots, self.stride, self.wdt,
+                              self.f, shared_w=self.shared, forced_idx=forced_idx, out=b.get("few"), ws=b.get("ws"),
+                              stream=stream)
+        return dict(y=y, topk_idx=idx, topk_w=w, x=x, residual=kept)
 
     def forward(self, x, forced_idx=None, ws=None, stream=None, slot_of_expert=None, bufs=None, residual=None):
         """x: device tensor [T, d].  Returns a dict of every intermediate and y [T, d].  With

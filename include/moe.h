@@ -250,6 +250,35 @@ MOE_API moe_status moe_combine(const void* y_perm, moe_dtype y_dtype, const floa
                                moe_dtype out, moe_stream s);
 
 /* ------------------------------------------------------------------------------------------
+ * moe_layer_few -- the whole layer for a few tokens (a decode step of a small batch) in two launches:
+ * moe_route, the experts and moe_combine, for layers whose experts are resident.
+ *   topk_idx, topk_w [T,k]: bitwise those of moe_route for the same x, w_router, bias and forced_idx
+ *   (finite logits; a NaN logit ranks below every other).  An id given twice in forced_idx counts with
+ *   the sum of its gates; ids outside [0, E) read as the nearest one, with unspecified gates.
+ *   y [T,d] act: y[t,:] = sum over the chosen experts of topk_w * expert output (+ the shared expert's),
+ *   rounded once.  h is rounded to bf16 when act is BF16 (quantised with FP8_B128 weights, as x is), every
+ *   sum is binary32, gates are applied to binary32 sums; the order of the sums is this call's own, so y
+ *   differs from the separate calls' by the roundings that fall otherwise.  It is the same for the
+ *   same inputs, and a token's row does not depend on the other tokens of the call's values.
+ *   An expert in slot MOE_SLOT_ELSEWHERE adds nothing; one in any other slot outside [0, n_slots) neither, and
+ *   sets the status word to 1.
+ * Types: x, w_router, y act; F32 weights with act F32; BF16, INT4_G128 and FP8_B128 weights with act BF16.
+ * Shapes: T <= MOE_FEW_TOKENS, k <= MOE_FEW_TOPK, d a multiple of 64, otherwise as moe_route and the slots;
+ * buffers start on 16 bytes, slots on 256 (slot_stride too).  y may be x.
+ * ws: moe_layer_few_workspace_bytes(...) bytes, zero-filled before its first use; its first 4 bytes are a sticky
+ * int32 status word (0 = no error).  One call at a time may use a workspace: two at once, also two replays of
+ * graphs that captured it, give undefined results and may set the status word to 2. */
+#define MOE_FEW_TOKENS 16
+#define MOE_FEW_TOPK 32
+/* never less than fewer tokens take; 0 for shapes that the call refuses */
+MOE_API size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k, int has_shared, moe_dtype w);
+MOE_API moe_status moe_layer_few(const void* x, moe_dtype act, int T, int d, int f, int E, int k, const void* w_router,
+                                 const float* bias, const int32_t* forced_idx, const int32_t* slot_of_expert,
+                                 int n_slots, const void* slot_pool, size_t slot_stride, moe_dtype w,
+                                 const void* shared_w, int32_t* topk_idx, float* topk_w, void* y, void* ws,
+                                 size_t ws_bytes, moe_stream s);
+
+/* ------------------------------------------------------------------------------------------
  * moe_add_rmsnorm -- the norm that stands before a layer, with the residual's addition (the pages
  * describe the layer from its input on; plain reading):
  *   h = x + residual, rounded to act (resid_out; without a residual h = x and resid_out is NULL),
