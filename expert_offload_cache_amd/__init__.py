@@ -14,7 +14,7 @@ import numpy as np
 from ._lib import (MOE_BF16, MOE_F32, MOE_FP8_B128, MOE_INT4_G128, MoeError, check, lib)
 
 __all__ = ["route", "permute", "permute_workspace", "permute_workspace_bytes", "route_permute", "expert_ffn_grouped", "expert_ffn_grouped_noalloc", "expert_ffn_fp8", "combine",
-           "layer_few", "layer_few_workspace_bytes", "add_rmsnorm", "quant_fp8", "gemm_fp8",
+           "layer_few", "layer_few_workspace_bytes", "add_rmsnorm", "quant_fp8", "gemm_fp8", "lora_linear", "lora_workspace_bytes",
            "slot_bytes", "pack_expert", "workspace_bytes", "hybrid_split", "SlotCache", "pinned_alloc", "pinned_free", "profile_enable",
            "profile_collect", "profile_results", "profile_reset", "MoeError", "WDT", "lib"]
 
@@ -314,6 +314,48 @@ def gemm_fp8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None):
     _on_current_device(a, a_scale, w, w_scale, out)
     check(lib().moe_gemm_fp8(_p(a), lda, _p(a_scale), M, K, _p(w), ldw, _p(w_scale), N, _p(out), ldc,
                              MOE_BF16 if out.dtype == torch.bfloat16 else MOE_F32, _s(stream)))
+    return out
+
+
+def lora_workspace_bytes(M: int, r: int) -> int:
+    return int(lib().moe_lora_workspace_bytes(M, r))
+
+
+def lora_linear(x, a, b, scale, adapter, w=None, base=None, rank=None, out=None, out_dtype=None, ws=None, stream=None):
+    """y [M, N] = x w^T + base + scale[i] * (x a[i]^T) b[i]^T, i = adapter[m], for each row m (moe_lora_linear).
+    x bf16 [M, K]; a bf16 [n, r, K], b bf16 [n, N, r], scale f32 [n], rank int32 [n] (None: r for all);
+    adapter int32 [M], a row's adapter or -1; w bf16 [N, K] (None: no projection); base [M, N] bfloat16 or float32
+    rows to add to (None: none).  out_dtype: bfloat16 (default) or float32; out may be base."""
+    torch = _torch()
+    M, K = x.shape
+    n, r = a.shape[:2]
+    N = b.shape[1]
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or bf16, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, not {out_dtype}")
+    for name, t in (("the result", out), ("base", base)):
+        if t is not None and t.dtype not in (bf16, f32):
+            raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    ldx, ldy = _rows("x", x, (M, K), bf16), _rows("out", out, (M, N), out.dtype)
+    ldw = _rows("w", w, (N, K), bf16) if w is not None else 0
+    ldb = _rows("base", base, (M, N), base.dtype) if base is not None else 0
+    _dense("a", a, (n, r, K), bf16)
+    _dense("b", b, (n, N, r), bf16)
+    _dense("scale", scale, (n,), f32)
+    _dense("adapter", adapter, (M,), i32)
+    if rank is not None:
+        _dense("rank", rank, (n,), i32)
+    if ws is None:
+        ws = torch.empty(lora_workspace_bytes(M, r) or 1, dtype=torch.uint8, device=x.device)
+    else:
+        _contig(ws)
+    _on_current_device(x, a, b, scale, adapter, w, base, rank, out, ws)
+    check(lib().moe_lora_linear(_p(x), ldx, M, K, _p(w), ldw, N, _p(base), ldb,
+                                MOE_F32 if base is None or base.dtype == f32 else MOE_BF16, _p(a), _p(b), r, n, _p(scale),
+                                _p(rank), _p(adapter), _p(out), ldy, MOE_BF16 if out.dtype == bf16 else MOE_F32, _p(ws),
+                                ws.nbytes, _s(stream)))
     return out
 
 

@@ -38,6 +38,9 @@ SIGNATURES = {
                               _sz, _vp, _vp]),
     "moe_quant_fp8": (_st, [_vp, _i32, _i32, _i32, _sz, _vp, _sz, _vp, _vp]),
     "moe_gemm_fp8": (_st, [_vp, _sz, _vp, _i32, _i32, _vp, _sz, _vp, _i32, _vp, _sz, _i32, _vp]),
+    "moe_lora_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_lora_linear": (_st, [_vp, _sz, _i32, _i32, _vp, _sz, _i32, _vp, _sz, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
+                              _sz, _i32, _vp, _sz, _vp]),
     "moe_prefill_gemv_tokens": (_i32, [_i32]),
     "moe_combine": (_st, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp]),
     "moe_decode_step": (_st, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _sz, _vp, _vp, _vp,

@@ -325,6 +325,29 @@ MOE_API moe_status moe_gemm_fp8(const void* a, size_t lda, const float* a_scale,
                                 size_t ldw, const float* w_scale, int N, void* c, size_t ldc, moe_dtype out,
                                 moe_stream s);
 
+/* moe_lora_linear -- a projection for rows of many requests, each with a low-rank adapter of its own or none:
+ *   y[m,:] = x[m,:] W^T + base[m,:] + scale[a] * (x[m,:] A_a[:rank_a]^T) B_a[:, :rank_a]^T,  a = adapter[m],
+ * without the first term where w is NULL, the second where base is NULL, the third where a is outside [0, n)
+ * (-1 by convention).  So it is a bf16 projection with adapters (w), or adds the adapters to the rows that
+ * another product left, moe_gemm_fp8 for one (base).
+ *   x [M,K], w [N,K] (rows are outputs), a [n,r,K], b [n,N,r] bf16, a and b contiguous; scale [n] binary32;
+ *   rank [n] int32 (clamped to [0, r]; what a and b hold beyond it is not used) or NULL: r for all;
+ *   adapter [M] int32; base [M,N] F32 or BF16; y [M,N] F32 or BF16, every row written, rounded once.
+ * Sums are binary32; x A^T is kept in binary32 (its second product takes it in bf16 parts: 16 bits of it for a
+ * BF16 result, all for an F32 one).  The order of the sums follows from M, N, K and r.  Rows with infinities or NaN, and
+ * adapters with them, touch no rows but their own.
+ * ldx, ldw, ldb, ldy: elements from a row to the next.  K, r, ldx and ldw multiples of 8; x, w, a, b and ws start on
+ * 16 bytes; any N; rows of base and y that start on 16 bytes are faster.  K up to 2^20, r up to MOE_LORA_MAX_RANK, N up to 2^22,
+ * M up to 2^21, n up to 2^20.  y may be base (same type and stride); no other overlap.
+ * ws: moe_lora_workspace_bytes(M, r) bytes, one call at a time. */
+#define MOE_LORA_MAX_RANK 512
+/* grows with M and with r; 0 where the call refuses them */
+MOE_API size_t moe_lora_workspace_bytes(int M, int r);
+MOE_API moe_status moe_lora_linear(const void* x, size_t ldx, int M, int K, const void* w, size_t ldw, int N,
+                                   const void* base, size_t ldb, moe_dtype base_dtype, const void* a, const void* b, int r,
+                                   int n, const float* scale, const int32_t* rank, const int32_t* adapter, void* y,
+                                   size_t ldy, moe_dtype out, void* ws, size_t ws_bytes, moe_stream s);
+
 /* ------------------------------------------------------------------------------------------
  * Expert-slot cache shared by all MoE layers (FreeToken linux guide, "MoE memory handling":
  * one LRU over GPU expert slots across the MoE layers, full pool in host RAM; a missed expert
