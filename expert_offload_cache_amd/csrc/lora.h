@@ -23,6 +23,7 @@ struct LoraArgs {
     void* y;                 // [M, N]
     size_t ldy;
     float* v;  // workspace [M, r]
+    bool wide;  // the rows of y and base start on 16 bytes
 };
 
 // an element of base or y
@@ -35,6 +36,8 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) { return f32_to_bf16(v); }
 
+// one row and a low rank: v is formed by the launch that uses it
+bool lora_alone(const LoraArgs& p);
 // v = scale A x for the rows that have an adapter
 moe_status lora_shrink(const LoraArgs& p, hipStream_t st);
 // y = x W^T + base + v B^T, any shape

@@ -136,78 +136,359 @@ __device__ __forceinline__ u32x4_t keep_first(u32x4_t v, int n) {
     return v;
 }
 
-// A wave takes 16 rows x 64 columns: 4 operand blocks of weight rows.  Row i of block b is column
-// 16 (i / 4) + 4 b + i % 4, so that a lane's results are 16 neighbouring columns of one row.
-template <typename OutT, typename BaseT, int PARTS>
-__global__ __launch_bounds__(256) void lora_rows_kernel(LoraArgs p) {
-    const int lane = threadIdx.x & 63, q = lane >> 4, r16 = lane & 15;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 64, m0 = (blockIdx.y * 4 + wv) * 16;
-    if (m0 >= p.M) return;  // the whole wave
-    const int m = m0 + r16;
-    int col[4];
+// ---- launch 2, few rows: the matrix streamed once -------------------------------------------------------
+// A workgroup takes 16 columns and all rows (16 MB of them); its 8 waves split the inputs, every load of 16 steps
+// of W on its way before the first product.  The adapters' second product is left to the vector units, a
+// row at a time (16 columns x r inputs: a wave reads them as they lie, 8 inputs a lane), so v stays
+// binary32.  ALONE: one row whose v is formed here too, by every workgroup for itself (A is small and in L2: one
+// launch less), NA blocks of 16 ranks.
+constexpr int kStreamWaves = 8;
+constexpr int kStreamRows = 64;
+
+template <typename OutT, typename BaseT, int MB, int NA>
+__global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs p) {
+    constexpr bool kAlone = NA > 0;
+    constexpr int B = 16, G = MB >= 3 ? 2 : 4;  // steps of W in flight; steps whose rows of x are read together
+    __shared__ float red[kStreamWaves][MB * 256];
+    __shared__ float delta[MB * 256];
+    __shared__ float vs[kAlone ? kStreamWaves + 1 : 1][kAlone ? NA * 16 : 1];
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n0 = blockIdx.x * 16;
+    f32x4_t acc[MB], av[kAlone ? NA : 1];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) col[b] = min(n0 + 16 * (r16 >> 2) + 4 * b + (r16 & 3), p.N - 1);
-    f32x4_t acc[4];
+    for (int i = 0; i < MB; ++i) acc[i] = zerof();
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[b] = zerof();
+    for (int i = 0; i < (kAlone ? NA : 1); ++i) av[i] = zerof();
+    const int only = kAlone ? __builtin_amdgcn_readfirstlane(adapter_of(p, 0)) : -1;
+    if (p.w || (kAlone && only >= 0)) {
+        const int nst = (p.K + 31) / 32, s0 = wv * nst / kStreamWaves, s1 = (wv + 1) * nst / kStreamWaves;
+        const uint16_t* wr = p.w ? p.w + (size_t)min(n0 + r16, p.N - 1) * p.ldw + 8 * q : nullptr;
+        const uint16_t *xr[MB], *ar[kAlone ? NA : 1];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) xr[i] = p.x + (size_t)min(16 * i + r16, p.M - 1) * p.ldx + 8 * q;
+        if constexpr (kAlone)
+#pragma unroll
+            for (int i = 0; i < NA; ++i) ar[i] = p.a + ((size_t)max(only, 0) * p.r + min(16 * i + r16, p.r - 1)) * p.K + 8 * q;
+        for (int sb = s0; sb < s1; sb += B) {
+            u32x4_t w[B];
+            if (p.w)
+#pragma unroll
+                for (int c = 0; c < B; ++c) {
+                    const int st = min(sb + c, s1 - 1);
+                    w[c] = st * 32 + 8 * q < p.K ? __builtin_nontemporal_load((const u32x4_t*)(wr + (size_t)st * 32)) : zero4();
+                }
+#pragma unroll
+            for (int g = 0; g < B; g += G) {
+                if (sb + g >= s1) break;
+                u32x4_t x[G][MB], a[G][kAlone ? NA : 1];
+#pragma unroll
+                for (int c = 0; c < G; ++c) {
+                    const int st = min(sb + g + c, s1 - 1);
+                    const bool in = st * 32 + 8 * q < p.K && sb + g + c < s1;
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) x[c][i] = in ? *(const u32x4_t*)(xr[i] + (size_t)st * 32) : zero4();
+                    if constexpr (kAlone)
+#pragma unroll
+                        for (int i = 0; i < NA; ++i) a[c][i] = in ? *(const u32x4_t*)(ar[i] + (size_t)st * 32) : zero4();
+                }
+#pragma unroll
+                for (int c = 0; c < G; ++c) {
+                    if (p.w && sb + g + c < s1)
+#pragma unroll
+                        for (int i = 0; i < MB; ++i) acc[i] = mfma_bf16(w[g + c], x[c][i], acc[i]);
+                    if constexpr (kAlone)
+#pragma unroll
+                        for (int i = 0; i < NA; ++i) av[i] = mfma_bf16(a[c][i], x[c][0], av[i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) *(f32x4_t*)&red[wv][i * 256 + r16 * 16 + 4 * q] = acc[i];
+    if constexpr (kAlone) {
+        if (r16 == 0)
+#pragma unroll
+            for (int i = 0; i < NA; ++i) *(f32x4_t*)&vs[wv][i * 16 + 4 * q] = av[i];
+        __syncthreads();
+        if (tid < NA * 16 && only >= 0) {
+            float s = vs[0][tid];
+#pragma unroll
+            for (int w = 1; w < kStreamWaves; ++w) s += vs[w][tid];
+            vs[kStreamWaves][tid] = p.scale[only] * s;
+        }
+        __syncthreads();
+    }
+    // rows wv, wv + 8, ...: lane l takes column l / 4 and inputs 8 (l % 4) .. + 7 of each 32
+    const int n = min(n0 + (lane >> 2), p.N - 1);
+    constexpr int F = 4;  // rows whose first operands are read together
+    for (int m0 = wv; m0 < p.M; m0 += kStreamWaves * F) {
+        int ad[F], rank[F];
+        float sum[F];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int m = m0 + f * kStreamWaves;
+            ad[f] = __builtin_amdgcn_readfirstlane(adapter_of(p, m));
+            rank[f] = ad[f] >= 0 ? rank_of(p, ad[f]) : 0;
+            sum[f] = 0.f;
+        }
+        int most = 0;
+#pragma unroll
+        for (int f = 0; f < F; ++f) most = max(most, rank[f]);
+        for (int k = 8 * (lane & 3); k < (most + 31) / 32 * 32; k += 32) {
+            u32x4_t b[F];
+            float4 lo[F], hi[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const bool in = k < rank[f];
+                const int m = m0 + f * kStreamWaves;
+                b[f] = in ? *(const u32x4_t*)(p.b + ((size_t)ad[f] * p.N + n) * p.r + k) : zero4();
+                const float4* v = kAlone ? (const float4*)&vs[kAlone ? kStreamWaves : 0][kAlone ? k : 0]
+                                         : (const float4*)(p.v + (size_t)m * p.r + k);
+                lo[f] = in ? v[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+                hi[f] = in ? v[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const float v[8] = {lo[f].x, lo[f].y, lo[f].z, lo[f].w, hi[f].x, hi[f].y, hi[f].z, hi[f].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // (places beyond the rank hold anything)
+                    sum[f] = k + 2 * i < rank[f] ? __builtin_fmaf(v[2 * i], bf16_lo(b[f][i]), sum[f]) : sum[f];
+                    sum[f] = k + 2 * i + 1 < rank[f] ? __builtin_fmaf(v[2 * i + 1], bf16_hi(b[f][i]), sum[f]) : sum[f];
+                }
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int m = m0 + f * kStreamWaves;
+            const float t = pair_sum2(pair_sum1(sum[f]));
+            if (m < p.M && (lane & 3) == 0) delta[m * 16 + (lane >> 2)] = t;
+        }
+    }
+    __syncthreads();
+    for (int o = tid; o < p.M * 16; o += 64 * kStreamWaves) {
+        const int m = o >> 4, c = n0 + (o & 15);
+        float s = red[0][o];
+#pragma unroll
+        for (int w = 1; w < kStreamWaves; ++w) s += red[w][o];
+        if (c < p.N) {
+            if (p.base) s += to_f32(((const BaseT*)p.base)[(size_t)m * p.ldb + c]);
+            ((OutT*)p.y)[(size_t)m * p.ldy + c] = from_f32<OutT>(s + delta[o]);
+        }
+    }
+}
+
+// ---- launch 2, many rows: tiles ---------------------------------------------------------------------------
+// A workgroup computes BN columns x BM rows; its WN x WM waves take equal parts.  Inputs advance 64 at a time
+// through a ring of R steps in LDS filled by direct-to-LDS loads: one barrier a step, after which the slot that the step
+// before has left is filled for step + R - 1.  A row's eight 16-byte chunks of a step lie on 128 bytes, chunk c at
+// position c ^ turn(row), so that no operand read meets a bank twice.
+// Operand row i of a wave's column block 4 g + b is column 64 g + 16 (i / 4) + 4 b + i % 4, so that a lane's results are
+// 16 neighbouring columns of a row, and four lanes' whole lines.
+// The adapters come last: each adapter of the tile's rows, 64 ranks at a time, with B and the parts of v in LDS in the
+// same layout.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(1))) void* gbl_ptr_t;
+__device__ __align__(16) const uint8_t g_no_inputs[16] = {};
+
+__device__ __forceinline__ int turn_n(int row) { return ((row >> 1) & 1) | ((row >> 4) & 3) << 1; }
+__device__ __forceinline__ int turn_m(int row) { return (row >> 1) & 7; }
+
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {  // at most N of this wave's loads in flight, its LDS reads done; then the others
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <typename OutT, typename BaseT, int BN, int BM, int WN, int WM, int R>
+__global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) {
+    constexpr int NW = WN * WM, RA = BN / WN / 16, CB = BM / WM / 16;
+    constexpr int PARTS = sizeof(OutT) == 2 ? 2 : 3;
+    constexpr int kStep = (BN + BM) * 128, kLoads = kStep / 1024 / NW;  // bytes of a step; a wave's 1 KB loads
+    static_assert(RA % 4 == 0 && kLoads * NW * 1024 == kStep, "tile shape");
+    static_assert(BN * 128 + PARTS * BM * 128 <= R * kStep, "B and the parts of v fit the ring");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_adapter[BM];
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wv % WN, wm = wv / WN;
+    // consecutive workgroups go to the XCDs in turn: each XCD takes a run of tiles, neighbours in n first
+    const int gx = (p.N + BN - 1) / BN, total = gx * ((p.M + BM - 1) / BM);
+    const int per = (total + 7) / 8, tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (tile >= total || (int)(blockIdx.x >> 3) >= per) return;
+    const int n0 = tile % gx * BN, m0 = tile / gx * BM;
+    for (int i = tid; i < BM; i += 64 * NW) s_adapter[i] = adapter_of(p, m0 + i);
+
+    f32x4_t acc[RA][CB];
+#pragma unroll
+    for (int i = 0; i < RA; ++i)
+#pragma unroll
+        for (int j = 0; j < CB; ++j) acc[i][j] = zerof();
+    // LDS byte of chunk q of a lane's operand row; chunk 4 + q is at ^ 64
+    int at_n[4], at_m[CB];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const int row = 16 * (r16 >> 2) + 4 * b + (r16 & 3);  // of a wave's first 64 columns
+        at_n[b] = (wn * RA * 16 + row) * 128 + ((q ^ turn_n(row)) << 4);
+    }
+#pragma unroll
+    for (int j = 0; j < CB; ++j) {
+        const int row = (wm * CB + j) * 16 + r16;
+        at_m[j] = (BN + row) * 128 + ((q ^ turn_m(row)) << 4);
+    }
+    // the products of what lies in `buf` over 32 of its inputs (half h) added to acc
+    auto multiply = [&](const uint8_t* buf, int h) __attribute__((always_inline)) {
+        u32x4_t b[CB];
+#pragma unroll
+        for (int j = 0; j < CB; ++j) b[j] = *(const u32x4_t*)(buf + (at_m[j] ^ (64 * h)));
+#pragma unroll
+        for (int i = 0; i < RA; ++i) {
+            const u32x4_t a = *(const u32x4_t*)(buf + (i / 4) * 64 * 128 + (at_n[i % 4] ^ (64 * h)));
+#pragma unroll
+            for (int j = 0; j < CB; ++j) acc[i][j] = mfma_bf16(a, b[j], acc[i][j]);
+        }
+    };
     if (p.w) {
-        const uint16_t* xr = p.x + (size_t)min(m, p.M - 1) * p.ldx;
-        for (int k = 8 * q; k < (p.K + 31) / 32 * 32; k += 32) {
-            const bool in = k < p.K;
-            const u32x4_t x = in ? *(const u32x4_t*)(xr + k) : zero4();
+        const int nst = (p.K + 63) / 64;
+        const uint16_t* src[kLoads];
+        int first[kLoads];  // this lane's first input of a step
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                acc[b] = mfma_bf16(in ? *(const u32x4_t*)(p.w + (size_t)col[b] * p.ldw + k) : zero4(), x, acc[b]);
+        for (int u = 0; u < kLoads; ++u) {
+            const int row = (wv * kLoads + u) * 8 + (lane >> 3);  // of the step's BN + BM
+            const bool is_n = row < BN;
+            const int r = is_n ? row : row - BN, c = (lane & 7) ^ (is_n ? turn_n(r) : turn_m(r));
+            first[u] = 8 * c;
+            src[u] = (is_n ? p.w + (size_t)min(n0 + r, p.N - 1) * p.ldw : p.x + (size_t)min(m0 + r, p.M - 1) * p.ldx) + 8 * c;
+        }
+        auto issue = [&](int ks, int slot) __attribute__((always_inline)) {
+            const int st = min(ks, nst - 1);  // past the end: the last step again, into a slot nobody reads
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const void* from = st * 64 + first[u] < p.K ? (const void*)(src[u] + (size_t)st * 64) : (const void*)g_no_inputs;
+                __builtin_amdgcn_global_load_lds((gbl_ptr_t)from, (lds_ptr_t)(smem + slot * kStep + (wv * kLoads + u) * 1024), 16, 0, 0);
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < R - 1; ++s) issue(s, s);
+        int slot = 0;
+        for (int ks = 0; ks < nst; ++ks) {
+            wait_and_meet<(R - 2) * kLoads>();  // step ks is there, and every wave has left step ks - 1
+            issue(ks + R - 1, slot == 0 ? R - 1 : slot - 1);
+            const uint8_t* buf = smem + slot * kStep;
+            multiply(buf, 0);
+            multiply(buf, 1);
+            slot = slot + 1 < R ? slot + 1 : 0;
         }
     }
-    const int mine = adapter_of(p, m);
-    uint64_t left = __ballot(mine >= 0);
-    while (left) {
-        const int a = __builtin_amdgcn_readfirstlane(__shfl(mine, __builtin_ctzll(left), 64));
-        left &= ~__ballot(mine == a);
-        const int rank = rank_of(p, a);
-        const bool on = mine == a;
-        f32x4_t d[4];
+    wait_and_meet<0>();  // the ring is free, s_adapter is written
+    int mine[CB];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) d[b] = zerof();
-        for (int k = 8 * q; k < (rank + 31) / 32 * 32; k += 32) {
-            float v[8];
-            const float4* vr = (const float4*)(p.v + (size_t)m * p.r + k);
-            const float4 lo = on && k < rank ? vr[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 hi = on && k < rank ? vr[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+    for (int j = 0; j < CB; ++j) mine[j] = s_adapter[(wm * CB + j) * 16 + r16];
+    for (int t0 = 0; t0 < BM; t0 += 64) {
+        // the adapters of these 64 rows that no row before them has
+        int who = lane < min(64, BM - t0) ? s_adapter[t0 + lane] : -1;
+        for (int i = 0; i < t0; ++i)
+            if (s_adapter[i] == who) who = -1;
+        uint64_t left = __ballot(who >= 0);
+        while (left) {
+            const int a = __builtin_amdgcn_readfirstlane(__shfl(who, __builtin_ctzll(left), 64));
+            left &= ~__ballot(who == a);
+            const int rank = rank_of(p, a);
+            for (int k0 = 0; k0 < rank; k0 += 64) {
+                const int halves = rank - k0 > 32 ? 2 : 1;
+                // B [BN, 64] and the parts of v [BM, 64]; places beyond the rank, and other adapters' rows, zero
+                for (int i = tid; i < BN * 8; i += 64 * NW) {
+                    const int row = i >> 3, c = i & 7, k = k0 + 8 * c;
+                    u32x4_t w = k < rank ? *(const u32x4_t*)(p.b + ((size_t)a * p.N + min(n0 + row, p.N - 1)) * p.r + k) : zero4();
+                    if (k + 8 > rank) w = keep_first(w, rank - k);
+                    *(u32x4_t*)(smem + row * 128 + ((c ^ turn_n(row)) << 4)) = w;
+                }
+                for (int i = tid; i < BM * 8; i += 64 * NW) {
+                    const int row = i >> 3, c = i & 7, k = k0 + 8 * c;
+                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (k < rank && s_adapter[row] == a) {
+                        const float4* from = (const float4*)(p.v + (size_t)(m0 + row) * p.r + k);
+                        const float4 lo = from[0], hi = from[1];
+                        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = k + i < rank ? v[i] : 0.f;
-            u32x4_t part[PARTS];
-            split_v<PARTS>(v, part);
+                        for (int e = 0; e < 8; ++e) v[e] = k + e < rank ? v[e] : 0.f;
+                    }
+                    u32x4_t part[PARTS];
+                    split_v<PARTS>(v, part);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                u32x4_t w = k < rank ? *(const u32x4_t*)(p.b + ((size_t)a * p.N + col[b]) * p.r + k) : zero4();
-                if (k + 8 > rank) w = keep_first(w, rank - k);
+                    for (int n = 0; n < PARTS; ++n)
+                        *(u32x4_t*)(smem + (BN + n * BM + row) * 128 + ((c ^ turn_m(row)) << 4)) = part[n];
+                }
+                __syncthreads();
 #pragma unroll
-                for (int n = 0; n < PARTS; ++n) d[b] = mfma_bf16(w, part[n], d[b]);
+                for (int j = 0; j < CB; ++j) {
+                    u32x4_t b[PARTS][2];
+#pragma unroll
+                    for (int n = 0; n < PARTS; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) b[n][h] = *(const u32x4_t*)(smem + n * BM * 128 + (at_m[j] ^ (64 * h)));
+                    const bool on = mine[j] == a;
+#pragma unroll
+                    for (int i = 0; i < RA; ++i) {
+                        f32x4_t d = zerof();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (h < halves) {
+                                const u32x4_t w = *(const u32x4_t*)(smem + (i / 4) * 64 * 128 + (at_n[i % 4] ^ (64 * h)));
+#pragma unroll
+                                for (int n = 0; n < PARTS; ++n) d = mfma_bf16(w, b[n][h], d);
+                            }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = on ? acc[i][j][e] + d[e] : acc[i][j][e];
+                    }
+                }
+                __syncthreads();
             }
         }
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[b][i] = on ? acc[b][i] + d[b][i] : acc[b][i];
     }
-    if (m >= p.M) return;
-    const int c0 = n0 + 16 * q;
-    const size_t at = (size_t)m * p.ldy + c0;
+    // a lane's 16 neighbouring columns of a row at a time
+    const bool wide = p.wide;
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int j = 0; j < CB; ++j) {
+        const int m = m0 + (wm * CB + j) * 16 + r16;
+        if (m >= p.M) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + 4 * b + i;
-            if (c < p.N) {
-                float s = acc[b][i];
-                if (p.base) s += to_f32(((const BaseT*)p.base)[(size_t)m * p.ldb + c]);
-                ((OutT*)p.y)[at + 4 * b + i] = from_f32<OutT>(s);
+        for (int g = 0; g < RA / 4; ++g) {
+            const int c0 = n0 + (wn * RA + 4 * g) * 16 + 16 * q;
+            if (c0 >= p.N) continue;
+            float s[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = acc[4 * g + e / 4][j][e % 4];
+            const BaseT* base = p.base ? (const BaseT*)p.base + (size_t)m * p.ldb + c0 : nullptr;
+            OutT* y = (OutT*)p.y + (size_t)m * p.ldy + c0;
+            if (wide && c0 + 16 <= p.N) {
+                if (base) {
+                    u32x4_t v[sizeof(BaseT)];
+#pragma unroll
+                    for (int e = 0; e < (int)sizeof(BaseT); ++e) v[e] = ((const u32x4_t*)base)[e];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        if constexpr (sizeof(BaseT) == 4) s[e] += as_f32(v[e / 4][e % 4]);
+                        else s[e] += e & 1 ? bf16_hi(v[e / 8][e % 8 / 2]) : bf16_lo(v[e / 8][e % 8 / 2]);
+                    }
+                }
+                if constexpr (sizeof(OutT) == 4) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ((float4*)y)[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        ((u32x4_t*)y)[e] = u32x4_t{bf16_pair(s[8 * e], s[8 * e + 1]), bf16_pair(s[8 * e + 2], s[8 * e + 3]),
+                                                   bf16_pair(s[8 * e + 4], s[8 * e + 5]), bf16_pair(s[8 * e + 6], s[8 * e + 7])};
+                }
+            } else {
+                for (int e = 0; e < 16; ++e)
+                    if (c0 + e < p.N) y[e] = from_f32<OutT>(s[e] + (base ? to_f32(base[e]) : 0.f));
             }
         }
+    }
 }
 
 template <int NM, int NR>
@@ -216,9 +497,49 @@ void launch_shrink(const LoraArgs& p, int turns, hipStream_t st) {
     lora_shrink_kernel<NM, NR><<<grid, 64 * kShrinkWaves, 0, st>>>(p);
 }
 
+template <typename OutT, typename BaseT>
+moe_status launch_stream(const LoraArgs& p, hipStream_t st) {
+    const unsigned grid = (unsigned)((p.N + 15) / 16);
+    if (lora_alone(p)) {
+        if (p.r <= 16) lora_stream_kernel<OutT, BaseT, 1, 1><<<grid, 64 * kStreamWaves, 0, st>>>(p);
+        else lora_stream_kernel<OutT, BaseT, 1, 2><<<grid, 64 * kStreamWaves, 0, st>>>(p);
+    } else if (p.M <= 16) lora_stream_kernel<OutT, BaseT, 1, 0><<<grid, 64 * kStreamWaves, 0, st>>>(p);
+    else if (p.M <= 32) lora_stream_kernel<OutT, BaseT, 2, 0><<<grid, 64 * kStreamWaves, 0, st>>>(p);
+    else if (p.M <= 48) lora_stream_kernel<OutT, BaseT, 3, 0><<<grid, 64 * kStreamWaves, 0, st>>>(p);
+    else lora_stream_kernel<OutT, BaseT, 4, 0><<<grid, 64 * kStreamWaves, 0, st>>>(p);
+    return MOE_OK;
+}
+
+int64_t tiles_of(const LoraArgs& p, int bn, int bm) { return ((int64_t)p.N + bn - 1) / bn * ((p.M + bm - 1) / bm); }
+
+template <typename OutT, typename BaseT, int BN, int BM, int WN, int WM, int R>
+moe_status launch_tile(const LoraArgs& p, hipStream_t st) {
+    constexpr int lds = R * (BN + BM) * 128;
+    auto kern = lora_tile_kernel<OutT, BaseT, BN, BM, WN, WM, R>;
+    MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+    kern<<<(unsigned)((tiles_of(p, BN, BM) + 7) / 8 * 8), 64 * WN * WM, lds, st>>>(p);
+    return MOE_OK;
+}
+
+template <typename OutT, typename BaseT>
+moe_status launch_tiles(const LoraArgs& p, hipStream_t st) {
+    if (p.w && tiles_of(p, 256, 256) >= 192) return launch_tile<OutT, BaseT, 256, 256, 2, 4, 2>(p, st);
+    if (tiles_of(p, 128, 128) >= 192) return launch_tile<OutT, BaseT, 128, 128, 2, 2, 3>(p, st);
+    return launch_tile<OutT, BaseT, 64, 64, 1, 4, 6>(p, st);
+}
+
+template <typename OutT>
+moe_status launch_rows(const LoraArgs& p, moe_dtype base, hipStream_t st) {
+    if (p.M <= kStreamRows) return base == MOE_BF16 ? launch_stream<OutT, uint16_t>(p, st) : launch_stream<OutT, float>(p, st);
+    return base == MOE_BF16 ? launch_tiles<OutT, uint16_t>(p, st) : launch_tiles<OutT, float>(p, st);
+}
+
 }  // namespace
 
+bool lora_alone(const LoraArgs& p) { return p.M == 1 && p.r <= 32; }
+
 moe_status lora_shrink(const LoraArgs& p, hipStream_t st) {
+    if (lora_alone(p)) return MOE_OK;
     ProfScope ps("lora_shrink", st);
     if (p.M <= 64) launch_shrink<1, 1>(p, std::min(p.M, 16), st);
     else if (p.r <= 16) launch_shrink<2, 1>(p, 1, st);
@@ -229,16 +550,9 @@ moe_status lora_shrink(const LoraArgs& p, hipStream_t st) {
 }
 
 moe_status lora_rows(const LoraArgs& p, moe_dtype base, moe_dtype out, hipStream_t st) {
-    const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 63) / 64));
-    ProfScope ps("lora_rows", st);
-    if (out == MOE_BF16) {
-        if (base == MOE_BF16) lora_rows_kernel<uint16_t, uint16_t, 2><<<grid, 256, 0, st>>>(p);
-        else lora_rows_kernel<uint16_t, float, 2><<<grid, 256, 0, st>>>(p);
-    } else {
-        if (base == MOE_BF16) lora_rows_kernel<float, uint16_t, 3><<<grid, 256, 0, st>>>(p);
-        else lora_rows_kernel<float, float, 3><<<grid, 256, 0, st>>>(p);
-    }
-    return check_launch("lora_rows");
+    ProfScope ps(p.M <= kStreamRows ? "lora_stream" : "lora_tile", st);
+    const moe_status e = out == MOE_BF16 ? launch_rows<uint16_t>(p, base, st) : launch_rows<float>(p, base, st);
+    return e == MOE_OK ? check_launch("lora_rows") : e;
 }
 
 }  // namespace moe

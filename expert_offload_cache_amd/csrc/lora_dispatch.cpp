@@ -34,7 +34,9 @@ moe_status moe_lora_linear(const void* x, size_t ldx, int M, int K, const void* 
     MOE_CHECK(ws_bytes >= moe_lora_workspace_bytes(M, r), MOE_ENOMEM, "%s: workspace of %zu bytes, need %zu", fn, ws_bytes,
               moe_lora_workspace_bytes(M, r));
     LoraArgs p{(const uint16_t*)x, ldx, M, K, (const uint16_t*)w, ldw, N, base, ldb, (const uint16_t*)a, (const uint16_t*)b, r, n,
-               scale, rank, adapter, y, ldy, (float*)ws};
+               scale, rank, adapter, y, ldy, (float*)ws, false};
+    auto starts_wide = [](const void* q, size_t ld, moe_dtype t) { return (((uintptr_t)q | ld * (t == MOE_F32 ? 4 : 2)) & 15) == 0; };
+    p.wide = starts_wide(y, ldy, out) && (!base || starts_wide(base, ldb, base_dtype));
     hipStream_t st = (hipStream_t)s;
     moe_status e = lora_shrink(p, st);
     if (e != MOE_OK) return e;
