@@ -35,78 +35,156 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& p, int m) {
 }
 __device__ __forceinline__ int rank_of(const LoraArgs& p, int a) { return p.rank ? min(max(p.rank[a], 0), p.r) : p.r; }
 
-// ---- launch 1 ---------------------------------------------------------------------------------------
-// A workgroup takes 16 * NM rows and NR blocks of 16 ranks; its 8 waves split the inputs.  The adapters of
-// its rows are taken one after the other (blockIdx.z, gridDim.z apart).
-constexpr int kShrinkWaves = 8;
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(1))) void* gbl_ptr_t;
+__device__ __align__(16) const uint8_t g_no_inputs[16] = {};
 
-template <int NM, int NR>
-__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs p) {
-    __shared__ float red[kShrinkWaves * NM * 256];
+// lane l's 16 bytes at `from` to 16 l bytes past `to` in LDS
+__device__ __forceinline__ void load_to_lds(const void* from, uint8_t* to) {
+    __builtin_amdgcn_global_load_lds((gbl_ptr_t)from, (lds_ptr_t)to, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {  // at most N of this wave's loads in flight, its LDS reads done; then the others
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// for every adapter of the rows' list (LDS, `rows` of them, -1: none), in order of appearance; uniform over the workgroup
+template <typename Body>
+__device__ __forceinline__ void for_adapters(const int* list, int rows, int lane, Body&& body) {
+    for (int t0 = 0; t0 < rows; t0 += 64) {
+        int who = lane < rows - t0 ? list[t0 + lane] : -1;
+        for (int i = 0; i < t0; ++i)
+            if (list[i] == who) who = -1;
+        uint64_t left = __ballot(who >= 0);
+        while (left) {
+            const int a = __builtin_amdgcn_readfirstlane(__shfl(who, __builtin_ctzll(left), 64));
+            left &= ~__ballot(who == a);
+            body(a);
+        }
+    }
+}
+
+// acc[j][i] += the products of 16 rows, block j of NA, with 16 rows of x, block i of NX, over the inputs of the steps
+// s0 .. s1 - 1 of 32.  The rows' loads run C steps ahead, those of x (which many workgroups read, from L2) G.
+// row(j), xrow(i): this lane's row of a block, nullptr a row of zeros.
+template <int NX, int NA, int C, int G, typename Row, typename XRow>
+__device__ __forceinline__ void stream_steps(int s0, int s1, int K, int q, Row&& row, XRow&& xrow, f32x4_t (&acc)[NA][NX]) {
+    static_assert(C % G == 0, "rings");
+    if (s0 >= s1) return;
+    const uint16_t *ar[NA], *xr[NX];
+    int xm[NX];  // 0: no row, the zeros again and again
+#pragma unroll
+    for (int i = 0; i < NA; ++i) ar[i] = row(i);
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+        xr[i] = xrow(i);
+        xm[i] = xr[i] ? -1 : 0;
+        xr[i] = xr[i] ? xr[i] : (const uint16_t*)g_no_inputs;
+    }
+    u32x4_t a[C][NA], x[G][NX];
+    // a step past the last repeats it, inputs past the last one repeat its chunk: neither is multiplied
+    auto at = [&](int s) __attribute__((always_inline)) { return min(min(s, s1 - 1) * 32 + 8 * q, K - 8); };
+    auto load_a = [&](int s, int c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i) a[c][i] = *(const u32x4_t*)(ar[i] + at(s));
+    };
+    auto load_x = [&](int s, int g) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) x[g][i] = *(const u32x4_t*)(xr[i] + (at(s) & xm[i]));
+    };
+    auto multiply = [&](int s, int c) __attribute__((always_inline)) {
+        const bool in = s * 32 + 8 * q < K;
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const u32x4_t v = in ? x[c % G][i] : zero4();
+#pragma unroll
+            for (int j = 0; j < NA; ++j) acc[j][i] = mfma_bf16(in ? a[c][j] : zero4(), v, acc[j][i]);
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < C; ++c) load_a(s0 + c, c);
+#pragma unroll
+    for (int c = 0; c < G; ++c) load_x(s0 + c, c);
+    int s = s0;
+    for (; s + C < s1; s += C)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            multiply(s + c, c);
+            load_a(s + c + C, c);
+            load_x(s + c + G, c % G);
+        }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (s + c < s1) multiply(s + c, c);
+        if (c + G < C) load_x(s + c + G, c % G);
+    }
+}
+
+// ---- launch 1 ---------------------------------------------------------------------------------------
+// A workgroup takes 16 * NM rows and NR blocks of 16 ranks; its NW waves split the inputs, each with the loads of C
+// steps on their way.  Of its rows' adapters it takes every Z-th.
+template <int NM, int NR, int NW, int C>
+__global__ __launch_bounds__(64 * NW, 4) void lora_shrink_kernel(LoraArgs p) {
+    __shared__ float red[NW * NM * NR * 256];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m0 = blockIdx.x * 16 * NM, r0 = blockIdx.y * 16 * NR;
-    // every wave: lane i holds row i's adapter (NM <= 4), `first` marks the rows whose adapter has not come before
+    // the first adapters' workgroups start last: beside those few that take a tile's second, not before them
+    const int Z = gridDim.z, z = Z - 1 - (int)blockIdx.z, m0 = blockIdx.x * 16 * NM, r0 = blockIdx.y * 16 * NR;
+    // every wave: lane i holds row i's adapter (NM <= 4)
     const int mine = lane < 16 * NM ? adapter_of(p, m0 + lane) : -1;
     uint64_t left = __ballot(mine >= 0);
     int turn = 0;
-    const int nst = (p.K + 31) / 32, s0 = wv * nst / kShrinkWaves, s1 = (wv + 1) * nst / kShrinkWaves;
+    const int nst = (p.K + 31) / 32, s0 = wv * nst / NW, s1 = (wv + 1) * nst / NW;
     while (left) {
         const int a = __builtin_amdgcn_readfirstlane(__shfl(mine, __builtin_ctzll(left), 64));
         const uint64_t rows = __ballot(mine == a);
         left &= ~rows;
-        if (turn++ % (int)gridDim.z != (int)blockIdx.z) continue;
+        if (turn++ % Z != z) continue;
         const int rank = rank_of(p, a);
         if (r0 >= rank) continue;
-        const uint16_t* A = p.a + (size_t)a * p.r * p.K;
-        f32x4_t acc[NM][NR];
+        const float scale = p.scale[a];
+        f32x4_t acc[NR][NM];
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+            for (int i = 0; i < NM; ++i) acc[j][i] = zerof();
+        stream_steps<NM, NR, C, C>(s0, s1, p.K, q,
+            [&](int j) __attribute__((always_inline)) { return p.a + ((size_t)a * p.r + min(r0 + 16 * j + r16, p.r - 1)) * p.K; },
+            [&](int i) __attribute__((always_inline)) {  // (other adapters' rows would be read for nothing)
+                const int m = 16 * i + r16;
+                return (rows >> m) & 1 ? p.x + (size_t)(m0 + m) * p.ldx : (const uint16_t*)nullptr;
+            }, acc);
 #pragma unroll
         for (int i = 0; i < NM; ++i)
 #pragma unroll
-            for (int j = 0; j < NR; ++j) acc[i][j] = zerof();
-        const uint16_t *xr[NM], *ar[NR];
-#pragma unroll
-        for (int i = 0; i < NM; ++i) xr[i] = p.x + (size_t)min(m0 + 16 * i + r16, p.M - 1) * p.ldx + 8 * q;
-#pragma unroll
-        for (int j = 0; j < NR; ++j) ar[j] = A + (size_t)min(r0 + 16 * j + r16, p.r - 1) * p.K + 8 * q;
-        constexpr int C = NM * NR <= 2 ? 8 : NM * NR <= 8 ? 4 : 2;  // steps whose loads are issued together
-        for (int s = s0; s < s1; s += C) {
-            u32x4_t vx[C][NM], va[C][NR];
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const bool in = s + c < s1 && (s + c) * 32 + 8 * q < p.K;
-#pragma unroll
-                for (int i = 0; i < NM; ++i) vx[c][i] = in ? *(const u32x4_t*)(xr[i] + (size_t)(s + c) * 32) : zero4();
-#pragma unroll
-                for (int j = 0; j < NR; ++j) va[c][j] = in ? *(const u32x4_t*)(ar[j] + (size_t)(s + c) * 32) : zero4();
-            }
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int j = 0; j < NR; ++j)
-#pragma unroll
-                    for (int i = 0; i < NM; ++i) acc[i][j] = mfma_bf16(va[c][j], vx[c][i], acc[i][j]);
-        }
-        const float scale = p.scale[a];
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < NM; ++i) *(f32x4_t*)&red[(wv * NM + i) * 256 + r16 * 16 + 4 * q] = acc[i][j];
-            __syncthreads();
-            for (int o = tid; o < NM * 256; o += 64 * kShrinkWaves) {
-                const int i = o >> 8, t = (o >> 4) & 15, c = r0 + 16 * j + (o & 15);
-                float s = red[o];
-#pragma unroll
-                for (int w = 1; w < kShrinkWaves; ++w) s += red[w * NM * 256 + o];
-                if (((rows >> (16 * i + t)) & 1) && c < rank) p.v[(size_t)(m0 + 16 * i + t) * p.r + c] = scale * s;
-            }
-        }
+            for (int j = 0; j < NR; ++j) *(f32x4_t*)&red[((wv * NM + i) * 16 + r16) * NR * 16 + j * 16 + 4 * q] = acc[j][i];
         __syncthreads();
+        for (int o = tid; o < NM * NR * 256; o += 64 * NW) {
+            const int m = o / (NR * 16), c = r0 + o % (NR * 16);
+            float s = red[o];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) s += red[w * NM * NR * 256 + o];
+            if (((rows >> m) & 1) && c < rank) p.v[(size_t)(m0 + m) * p.r + c] = scale * s;
+        }
+        if (left) __syncthreads();
     }
 }
 
 // ---- launch 2 ---------------------------------------------------------------------------------------
+// 8 values of v from input k on, those beyond the rank zero
+__device__ __forceinline__ void load_v(const LoraArgs& p, int m, int k, int rank, float (&v)[8]) {
+    const float4* from = (const float4*)(p.v + (size_t)m * p.r + k);
+    const float4 lo = from[0], hi = from[1];
+    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = k + e < rank ? v[e] : 0.f;
+}
+
 // 8 values of v as bf16 parts
 template <int PARTS>
 __device__ __forceinline__ void split_v(const float (&v)[8], u32x4_t (&part)[PARTS]) {
@@ -136,99 +214,111 @@ __device__ __forceinline__ u32x4_t keep_first(u32x4_t v, int n) {
     return v;
 }
 
+// 16 neighbouring columns of a row: base is asked for at once, added at the store
+template <typename OutT, typename BaseT>
+struct Columns {
+    const LoraArgs& p;
+    const int m, c0;
+    const bool whole;
+    u32x4_t base[sizeof(BaseT)];
+    __device__ __forceinline__ Columns(const LoraArgs& p, int m, int c0)
+        : p(p), m(m), c0(c0), whole(p.wide && m < p.M && c0 + 16 <= p.N) {
+        if (!p.base) return;
+        const u32x4_t* from = (const u32x4_t*)((const BaseT*)p.base + (size_t)m * p.ldb + c0);
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(BaseT); ++e) base[e] = whole ? from[e] : zero4();
+    }
+    __device__ __forceinline__ void store(float (&s)[16]) const {
+        OutT* y = (OutT*)p.y + (size_t)m * p.ldy + c0;
+        if (whole) {
+            if (p.base)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if constexpr (sizeof(BaseT) == 4) s[e] += as_f32(base[e / 4][e % 4]);
+                    else s[e] += e & 1 ? bf16_hi(base[e / 8][e % 8 / 2]) : bf16_lo(base[e / 8][e % 8 / 2]);
+                }
+            if constexpr (sizeof(OutT) == 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ((float4*)y)[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    ((u32x4_t*)y)[e] = u32x4_t{bf16_pair(s[8 * e], s[8 * e + 1]), bf16_pair(s[8 * e + 2], s[8 * e + 3]),
+                                               bf16_pair(s[8 * e + 4], s[8 * e + 5]), bf16_pair(s[8 * e + 6], s[8 * e + 7])};
+            }
+        } else if (m < p.M) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (c0 + e < p.N) {
+                    const float b = p.base ? to_f32(((const BaseT*)p.base)[(size_t)m * p.ldb + c0 + e]) : 0.f;
+                    y[e] = from_f32<OutT>(s[e] + b);
+                }
+        }
+    }
+};
+
 // ---- launch 2, few rows: the matrix streamed once -------------------------------------------------------
-// A workgroup takes 16 columns and all rows (16 MB of them); its 8 waves split the inputs, every load of 16 steps
-// of W on its way before the first product.  The adapters' second product is left to the vector units, a
-// row at a time (16 columns x r inputs: a wave reads them as they lie, 8 inputs a lane), so v stays
-// binary32.  ALONE: one row whose v is formed here too, by every workgroup for itself (A is small and in L2: one
-// launch less), NA blocks of 16 ranks.
-constexpr int kStreamWaves = 8;
+// A workgroup takes 16 columns and all rows (16 MB of them).  8 of its 16 waves split the inputs of x W^T, the loads of
+// 8 steps of W on their way; meanwhile the other 8 (all 16 without W) form the adapters' second product on
+// the vector units, a row at a time: 16 columns x r inputs, a wave reads them as they lie, and v stays binary32.
+// ALONE: one row whose v is formed here too, by every workgroup for itself (A is small and in L2: one launch less), by the
+// other 8 waves; NA blocks of 16 ranks.
+constexpr int kStreamWaves = 16;
 constexpr int kStreamRows = 64;
 
 template <typename OutT, typename BaseT, int MB, int NA>
 __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs p) {
     constexpr bool kAlone = NA > 0;
-    constexpr int B = 16, G = MB >= 3 ? 2 : 4;  // steps of W in flight; steps whose rows of x are read together
-    __shared__ float red[kStreamWaves][MB * 256];
+    constexpr int H = kStreamWaves / 2;
+    __shared__ float red[H][MB * 256];
     __shared__ float delta[MB * 256];
-    __shared__ float vs[kAlone ? kStreamWaves + 1 : 1][kAlone ? NA * 16 : 1];
+    __shared__ __align__(16) float vs[kAlone ? H + 1 : 1][kAlone ? NA * 16 : 1];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 16;
-    f32x4_t acc[MB], av[kAlone ? NA : 1];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) acc[i] = zerof();
-#pragma unroll
-    for (int i = 0; i < (kAlone ? NA : 1); ++i) av[i] = zerof();
+    const int n0 = blockIdx.x * 16, nst = (p.K + 31) / 32;
     const int only = kAlone ? __builtin_amdgcn_readfirstlane(adapter_of(p, 0)) : -1;
-    if (p.w || (kAlone && only >= 0)) {
-        const int nst = (p.K + 31) / 32, s0 = wv * nst / kStreamWaves, s1 = (wv + 1) * nst / kStreamWaves;
-        const uint16_t* wr = p.w ? p.w + (size_t)min(n0 + r16, p.N - 1) * p.ldw + 8 * q : nullptr;
-        const uint16_t *xr[MB], *ar[kAlone ? NA : 1];
+    auto x_row = [&](int i) __attribute__((always_inline)) { return p.x + (size_t)min(16 * i + r16, p.M - 1) * p.ldx; };
+    if (wv < H && p.w) {
+        f32x4_t acc[1][MB];
 #pragma unroll
-        for (int i = 0; i < MB; ++i) xr[i] = p.x + (size_t)min(16 * i + r16, p.M - 1) * p.ldx + 8 * q;
-        if constexpr (kAlone)
+        for (int i = 0; i < MB; ++i) acc[0][i] = zerof();
+        stream_steps<MB, 1, 8, MB <= 2 ? 8 : MB == 3 ? 4 : 2>(wv * nst / H, (wv + 1) * nst / H, p.K, q,
+            [&](int) __attribute__((always_inline)) { return p.w + (size_t)min(n0 + r16, p.N - 1) * p.ldw; }, x_row, acc);
 #pragma unroll
-            for (int i = 0; i < NA; ++i) ar[i] = p.a + ((size_t)max(only, 0) * p.r + min(16 * i + r16, p.r - 1)) * p.K + 8 * q;
-        for (int sb = s0; sb < s1; sb += B) {
-            u32x4_t w[B];
-            if (p.w)
-#pragma unroll
-                for (int c = 0; c < B; ++c) {
-                    const int st = min(sb + c, s1 - 1);
-                    w[c] = st * 32 + 8 * q < p.K ? __builtin_nontemporal_load((const u32x4_t*)(wr + (size_t)st * 32)) : zero4();
-                }
-#pragma unroll
-            for (int g = 0; g < B; g += G) {
-                if (sb + g >= s1) break;
-                u32x4_t x[G][MB], a[G][kAlone ? NA : 1];
-#pragma unroll
-                for (int c = 0; c < G; ++c) {
-                    const int st = min(sb + g + c, s1 - 1);
-                    const bool in = st * 32 + 8 * q < p.K && sb + g + c < s1;
-#pragma unroll
-                    for (int i = 0; i < MB; ++i) x[c][i] = in ? *(const u32x4_t*)(xr[i] + (size_t)st * 32) : zero4();
-                    if constexpr (kAlone)
-#pragma unroll
-                        for (int i = 0; i < NA; ++i) a[c][i] = in ? *(const u32x4_t*)(ar[i] + (size_t)st * 32) : zero4();
-                }
-#pragma unroll
-                for (int c = 0; c < G; ++c) {
-                    if (p.w && sb + g + c < s1)
-#pragma unroll
-                        for (int i = 0; i < MB; ++i) acc[i] = mfma_bf16(w[g + c], x[c][i], acc[i]);
-                    if constexpr (kAlone)
-#pragma unroll
-                        for (int i = 0; i < NA; ++i) av[i] = mfma_bf16(a[c][i], x[c][0], av[i]);
-                }
-            }
-        }
+        for (int i = 0; i < MB; ++i) *(f32x4_t*)&red[wv][i * 256 + r16 * 16 + 4 * q] = acc[0][i];
     }
-#pragma unroll
-    for (int i = 0; i < MB; ++i) *(f32x4_t*)&red[wv][i * 256 + r16 * 16 + 4 * q] = acc[i];
     if constexpr (kAlone) {
-        if (r16 == 0)
+        if (wv >= H && only >= 0) {
+            f32x4_t acc[NA][1];
 #pragma unroll
-            for (int i = 0; i < NA; ++i) *(f32x4_t*)&vs[wv][i * 16 + 4 * q] = av[i];
+            for (int i = 0; i < NA; ++i) acc[i][0] = zerof();
+            stream_steps<1, NA, 8, 8>((wv - H) * nst / H, (wv - H + 1) * nst / H, p.K, q,
+                [&](int i) __attribute__((always_inline)) { return p.a + ((size_t)only * p.r + min(16 * i + r16, p.r - 1)) * p.K; }, x_row, acc);
+            if (r16 == 0)
+#pragma unroll
+                for (int i = 0; i < NA; ++i) *(f32x4_t*)&vs[wv - H][i * 16 + 4 * q] = acc[i][0];
+        }
         __syncthreads();
         if (tid < NA * 16 && only >= 0) {
             float s = vs[0][tid];
 #pragma unroll
-            for (int w = 1; w < kStreamWaves; ++w) s += vs[w][tid];
-            vs[kStreamWaves][tid] = p.scale[only] * s;
+            for (int w = 1; w < H; ++w) s += vs[w][tid];
+            vs[H][tid] = p.scale[only] * s;
         }
         __syncthreads();
     }
-    // rows wv, wv + 8, ...: lane l takes column l / 4 and inputs 8 (l % 4) .. + 7 of each 32
+    // rows first, first + step, ...: lane l takes column l / 4 and inputs 8 (l % 4) .. + 7 of each 32
+    constexpr int F = MB >= 3 ? 4 : MB;  // rows whose operands are read together
+    const int first = p.w && !kAlone ? wv - H : wv, step = p.w && !kAlone ? H : kStreamWaves;
     const int n = min(n0 + (lane >> 2), p.N - 1);
-    constexpr int F = 4;  // rows whose first operands are read together
-    for (int m0 = wv; m0 < p.M; m0 += kStreamWaves * F) {
+    for (int m0 = first; m0 >= 0 && m0 < p.M; m0 += step * F) {
         int ad[F], rank[F];
         float sum[F];
 #pragma unroll
+        for (int f = 0; f < F; ++f) ad[f] = adapter_of(p, m0 + f * step);
+#pragma unroll
         for (int f = 0; f < F; ++f) {
-            const int m = m0 + f * kStreamWaves;
-            ad[f] = __builtin_amdgcn_readfirstlane(adapter_of(p, m));
+            ad[f] = __builtin_amdgcn_readfirstlane(ad[f]);
             rank[f] = ad[f] >= 0 ? rank_of(p, ad[f]) : 0;
             sum[f] = 0.f;
         }
@@ -241,10 +331,9 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 const bool in = k < rank[f];
-                const int m = m0 + f * kStreamWaves;
+                const int m = m0 + f * step;
                 b[f] = in ? *(const u32x4_t*)(p.b + ((size_t)ad[f] * p.N + n) * p.r + k) : zero4();
-                const float4* v = kAlone ? (const float4*)&vs[kAlone ? kStreamWaves : 0][kAlone ? k : 0]
-                                         : (const float4*)(p.v + (size_t)m * p.r + k);
+                const float4* v = kAlone ? (const float4*)&vs[kAlone ? H : 0][kAlone ? k : 0] : (const float4*)(p.v + (size_t)m * p.r + k);
                 lo[f] = in ? v[0] : make_float4(0.f, 0.f, 0.f, 0.f);
                 hi[f] = in ? v[1] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -260,7 +349,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            const int m = m0 + f * kStreamWaves;
+            const int m = m0 + f * step;
             const float t = pair_sum2(pair_sum1(sum[f]));
             if (m < p.M && (lane & 3) == 0) delta[m * 16 + (lane >> 2)] = t;
         }
@@ -268,12 +357,117 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
     __syncthreads();
     for (int o = tid; o < p.M * 16; o += 64 * kStreamWaves) {
         const int m = o >> 4, c = n0 + (o & 15);
-        float s = red[0][o];
+        float s = 0.f;
+        if (p.w) {
+            s = red[0][o];
 #pragma unroll
-        for (int w = 1; w < kStreamWaves; ++w) s += red[w][o];
+            for (int w = 1; w < H; ++w) s += red[w][o];
+        }
         if (c < p.N) {
             if (p.base) s += to_f32(((const BaseT*)p.base)[(size_t)m * p.ldb + c]);
             ((OutT*)p.y)[(size_t)m * p.ldy + c] = from_f32<OutT>(s + delta[o]);
+        }
+    }
+}
+
+// ---- launch 2, many rows and no matrix -------------------------------------------------------------------
+// A workgroup takes 64 rows and 512 columns, its 4 waves 64 columns at a time.  The rows' v lies in LDS as bf16 parts, 64
+// ranks at a time (row's chunk c at c ^ row % 8); B and base come straight to registers.  Columns in the order
+// of the tiles below, so that a lane holds 16 neighbouring ones.
+constexpr int kAddCols = 512;
+
+template <typename OutT, typename BaseT>
+__global__ __launch_bounds__(256) void lora_add_kernel(LoraArgs p) {
+    constexpr int PARTS = sizeof(OutT) == 2 ? 2 : 3;
+    __shared__ __align__(16) uint8_t parts[PARTS * 64 * 128];
+    __shared__ int s_adapter[64], s_rank[64];
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m0 = blockIdx.y * 64;
+    if (tid < 64) {
+        const int a = adapter_of(p, m0 + tid);
+        s_adapter[tid] = a;
+        s_rank[tid] = a >= 0 ? rank_of(p, a) : 0;
+    }
+    __syncthreads();
+    auto stage = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = tid; i < 64 * 8; i += 256) {
+            const int row = i >> 3, c = i & 7, k = k0 + 8 * c;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (k < s_rank[row]) load_v(p, m0 + row, k, s_rank[row], v);
+            u32x4_t part[PARTS];
+            split_v<PARTS>(v, part);
+#pragma unroll
+            for (int n = 0; n < PARTS; ++n) *(u32x4_t*)(parts + (n * 64 + row) * 128 + ((c ^ (row & 7)) << 4)) = part[n];
+        }
+        __syncthreads();
+    };
+    int mine[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine[j] = s_adapter[16 * j + r16];
+    stage(0);
+    for (int g = wv; g < kAddCols / 64; g += 4) {
+        const int n0 = blockIdx.x * kAddCols + 64 * g;  // (past the end: nothing is stored)
+        const Columns<OutT, BaseT> out[4] = {{p, m0 + r16, n0 + 16 * q}, {p, m0 + 16 + r16, n0 + 16 * q},
+                                             {p, m0 + 32 + r16, n0 + 16 * q}, {p, m0 + 48 + r16, n0 + 16 * q}};
+        f32x4_t acc[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] = zerof();
+        for (int k0 = 0; k0 < p.r; k0 += 64) {
+            if (p.r > 64) {
+                __syncthreads();
+                stage(k0);
+            }
+            for_adapters(s_adapter, 64, lane, [&](int a) __attribute__((always_inline)) {
+                const int rank = p.rank ? rank_of(p, a) : p.r;
+                if (k0 >= rank) return;
+                u32x4_t b[4][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = k0 + 32 * h + 8 * q;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = min(n0 + 16 * (r16 >> 2) + 4 * i + (r16 & 3), p.N - 1);
+                        b[i][h] = *(const u32x4_t*)(p.b + ((size_t)a * p.N + n) * p.r + min(k, p.r - 8));
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[i][h] = keep_first(b[i][h], rank - (k0 + 32 * h + 8 * q));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool on = mine[j] == a;
+                    if (!__ballot(on)) continue;
+                    f32x4_t d[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = zerof();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (k0 + 32 * h >= rank) break;
+#pragma unroll
+                        for (int n = 0; n < PARTS; ++n) {
+                            const u32x4_t v = *(const u32x4_t*)(parts + (n * 64 + 16 * j + r16) * 128 + (((4 * h + q) ^ (r16 & 7)) << 4));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) d[i] = mfma_bf16(b[i][h], v, d[i]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][i][e] = on ? acc[j][i][e] + d[i][e] : acc[j][i][e];
+                }
+            });
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float s[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = acc[j][e / 4][e % 4];
+            out[j].store(s);
         }
     }
 }
@@ -287,21 +481,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
 // 16 neighbouring columns of a row, and four lanes' whole lines.
 // The adapters come last: each adapter of the tile's rows, 64 ranks at a time, with B and the parts of v in LDS in the
 // same layout.
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-typedef __attribute__((address_space(1))) void* gbl_ptr_t;
-__device__ __align__(16) const uint8_t g_no_inputs[16] = {};
-
 __device__ __forceinline__ int turn_n(int row) { return ((row >> 1) & 1) | ((row >> 4) & 3) << 1; }
 __device__ __forceinline__ int turn_m(int row) { return (row >> 1) & 7; }
-
-template <int N>
-__device__ __forceinline__ void wait_and_meet() {  // at most N of this wave's loads in flight, its LDS reads done; then the others
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 template <typename OutT, typename BaseT, int BN, int BM, int WN, int WM, int R>
 __global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) {
@@ -367,7 +548,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) 
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 const void* from = st * 64 + first[u] < p.K ? (const void*)(src[u] + (size_t)st * 64) : (const void*)g_no_inputs;
-                __builtin_amdgcn_global_load_lds((gbl_ptr_t)from, (lds_ptr_t)(smem + slot * kStep + (wv * kLoads + u) * 1024), 16, 0, 0);
+                load_to_lds(from, smem + slot * kStep + (wv * kLoads + u) * 1024);
             }
         };
 #pragma unroll
@@ -386,15 +567,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) 
     int mine[CB];
 #pragma unroll
     for (int j = 0; j < CB; ++j) mine[j] = s_adapter[(wm * CB + j) * 16 + r16];
-    for (int t0 = 0; t0 < BM; t0 += 64) {
-        // the adapters of these 64 rows that no row before them has
-        int who = lane < min(64, BM - t0) ? s_adapter[t0 + lane] : -1;
-        for (int i = 0; i < t0; ++i)
-            if (s_adapter[i] == who) who = -1;
-        uint64_t left = __ballot(who >= 0);
-        while (left) {
-            const int a = __builtin_amdgcn_readfirstlane(__shfl(who, __builtin_ctzll(left), 64));
-            left &= ~__ballot(who == a);
+    for_adapters(s_adapter, BM, lane, [&](int a) __attribute__((always_inline)) {
             const int rank = rank_of(p, a);
             for (int k0 = 0; k0 < rank; k0 += 64) {
                 const int halves = rank - k0 > 32 ? 2 : 1;
@@ -408,13 +581,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) 
                 for (int i = tid; i < BM * 8; i += 64 * NW) {
                     const int row = i >> 3, c = i & 7, k = k0 + 8 * c;
                     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if (k < rank && s_adapter[row] == a) {
-                        const float4* from = (const float4*)(p.v + (size_t)(m0 + row) * p.r + k);
-                        const float4 lo = from[0], hi = from[1];
-                        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = k + e < rank ? v[e] : 0.f;
-                    }
+                    if (k < rank && s_adapter[row] == a) load_v(p, m0 + row, k, rank, v);
                     u32x4_t part[PARTS];
                     split_v<PARTS>(v, part);
 #pragma unroll
@@ -446,55 +613,23 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) 
                 }
                 __syncthreads();
             }
-        }
-    }
-    // a lane's 16 neighbouring columns of a row at a time
-    const bool wide = p.wide;
+    });
 #pragma unroll
-    for (int j = 0; j < CB; ++j) {
-        const int m = m0 + (wm * CB + j) * 16 + r16;
-        if (m >= p.M) continue;
+    for (int j = 0; j < CB; ++j)
 #pragma unroll
         for (int g = 0; g < RA / 4; ++g) {
-            const int c0 = n0 + (wn * RA + 4 * g) * 16 + 16 * q;
-            if (c0 >= p.N) continue;
+            const Columns<OutT, BaseT> out(p, m0 + (wm * CB + j) * 16 + r16, n0 + (wn * RA + 4 * g) * 16 + 16 * q);
             float s[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = acc[4 * g + e / 4][j][e % 4];
-            const BaseT* base = p.base ? (const BaseT*)p.base + (size_t)m * p.ldb + c0 : nullptr;
-            OutT* y = (OutT*)p.y + (size_t)m * p.ldy + c0;
-            if (wide && c0 + 16 <= p.N) {
-                if (base) {
-                    u32x4_t v[sizeof(BaseT)];
-#pragma unroll
-                    for (int e = 0; e < (int)sizeof(BaseT); ++e) v[e] = ((const u32x4_t*)base)[e];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if constexpr (sizeof(BaseT) == 4) s[e] += as_f32(v[e / 4][e % 4]);
-                        else s[e] += e & 1 ? bf16_hi(v[e / 8][e % 8 / 2]) : bf16_lo(v[e / 8][e % 8 / 2]);
-                    }
-                }
-                if constexpr (sizeof(OutT) == 4) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) ((float4*)y)[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        ((u32x4_t*)y)[e] = u32x4_t{bf16_pair(s[8 * e], s[8 * e + 1]), bf16_pair(s[8 * e + 2], s[8 * e + 3]),
-                                                   bf16_pair(s[8 * e + 4], s[8 * e + 5]), bf16_pair(s[8 * e + 6], s[8 * e + 7])};
-                }
-            } else {
-                for (int e = 0; e < 16; ++e)
-                    if (c0 + e < p.N) y[e] = from_f32<OutT>(s[e] + (base ? to_f32(base[e]) : 0.f));
-            }
+            out.store(s);
         }
-    }
 }
 
-template <int NM, int NR>
-void launch_shrink(const LoraArgs& p, int turns, hipStream_t st) {
-    const dim3 grid((unsigned)((p.M + 16 * NM - 1) / (16 * NM)), (unsigned)((p.r + 16 * NR - 1) / (16 * NR)), (unsigned)turns);
-    lora_shrink_kernel<NM, NR><<<grid, 64 * kShrinkWaves, 0, st>>>(p);
+template <int NM, int NR, int NW, int C>
+void launch_shrink(const LoraArgs& p, int z, hipStream_t st) {
+    const dim3 grid((unsigned)((p.M + 16 * NM - 1) / (16 * NM)), (unsigned)((p.r + 16 * NR - 1) / (16 * NR)), (unsigned)z);
+    lora_shrink_kernel<NM, NR, NW, C><<<grid, 64 * NW, 0, st>>>(p);
 }
 
 template <typename OutT, typename BaseT>
@@ -523,7 +658,11 @@ moe_status launch_tile(const LoraArgs& p, hipStream_t st) {
 
 template <typename OutT, typename BaseT>
 moe_status launch_tiles(const LoraArgs& p, hipStream_t st) {
-    if (p.w && tiles_of(p, 256, 256) >= 192) return launch_tile<OutT, BaseT, 256, 256, 2, 4, 2>(p, st);
+    if (!p.w) {
+        lora_add_kernel<OutT, BaseT><<<dim3((unsigned)((p.N + kAddCols - 1) / kAddCols), (unsigned)((p.M + 63) / 64)), 256, 0, st>>>(p);
+        return MOE_OK;
+    }
+    if (tiles_of(p, 256, 256) >= 192) return launch_tile<OutT, BaseT, 256, 256, 2, 4, 2>(p, st);
     if (tiles_of(p, 128, 128) >= 192) return launch_tile<OutT, BaseT, 128, 128, 2, 2, 3>(p, st);
     return launch_tile<OutT, BaseT, 64, 64, 1, 4, 6>(p, st);
 }
@@ -541,16 +680,15 @@ bool lora_alone(const LoraArgs& p) { return p.M == 1 && p.r <= 32; }
 moe_status lora_shrink(const LoraArgs& p, hipStream_t st) {
     if (lora_alone(p)) return MOE_OK;
     ProfScope ps("lora_shrink", st);
-    if (p.M <= 64) launch_shrink<1, 1>(p, std::min(p.M, 16), st);
-    else if (p.r <= 16) launch_shrink<2, 1>(p, 1, st);
-    else if (p.r <= 32) launch_shrink<2, 2>(p, 1, st);
-    else if (p.r <= 64) launch_shrink<2, 4>(p, 1, st);
-    else launch_shrink<2, 8>(p, 1, st);
+    const int blocks = (p.M + 15) / 16 * ((p.r + 15) / 16);
+    if (p.M <= kStreamRows) launch_shrink<1, 1, 16, 4>(p, std::min(std::min(p.M, 16), p.n), st);
+    else if (blocks < 256) launch_shrink<1, 1, 16, 4>(p, std::min(p.n, 2), st);
+    else launch_shrink<2, 2, 8, 4>(p, std::min(p.n, 2), st);
     return check_launch("lora_shrink");
 }
 
 moe_status lora_rows(const LoraArgs& p, moe_dtype base, moe_dtype out, hipStream_t st) {
-    ProfScope ps(p.M <= kStreamRows ? "lora_stream" : "lora_tile", st);
+    ProfScope ps(p.M <= kStreamRows ? "lora_stream" : p.w ? "lora_tile" : "lora_add", st);
     const moe_status e = out == MOE_BF16 ? launch_rows<uint16_t>(p, base, st) : launch_rows<float>(p, base, st);
     return e == MOE_OK ? check_launch("lora_rows") : e;
 }
