@@ -1189,6 +1189,8 @@ extern "C" moe_status moe_layer_few(const void* x, moe_dtype act, int T, int d, 
               "%s: slot pool / shared expert must be 256-byte aligned", fn);
     MOE_CHECK((((uintptr_t)x | (uintptr_t)w_router | (uintptr_t)y | (uintptr_t)ws) & 15) == 0, MOE_EINVAL,
               "%s: x, w_router, y and ws must be 16-byte aligned", fn);
+    MOE_CHECK((((uintptr_t)bias | (uintptr_t)forced_idx | (uintptr_t)slot_of_expert | (uintptr_t)topk_idx | (uintptr_t)topk_w) & 3) == 0,
+              MOE_EINVAL, "%s: bias, forced_idx, slot_of_expert, topk_idx and topk_w must be 4-byte aligned", fn);
     const FewLayout l = few_layout(T, d, f, E, k, shared_w != nullptr, w);
     MOE_CHECK(ws_bytes >= l.total, MOE_ENOMEM, "%s: workspace of %zu bytes, need %zu", fn, ws_bytes, l.total);
     uint8_t* p = (uint8_t*)ws;

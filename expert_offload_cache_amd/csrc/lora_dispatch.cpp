@@ -30,6 +30,9 @@ moe_status moe_lora_linear(const void* x, size_t ldx, int M, int K, const void* 
     MOE_CHECK(ldy >= (size_t)N && (!base || ldb >= (size_t)N), MOE_EINVAL, "%s: rows of y and base must be at least N apart", fn);
     MOE_CHECK((((uintptr_t)x | (uintptr_t)w | (uintptr_t)a | (uintptr_t)b | (uintptr_t)ws) & 15) == 0, MOE_EINVAL,
               "%s: x, w, a, b and ws must be 16-byte aligned", fn);
+    MOE_CHECK((((uintptr_t)scale | (uintptr_t)rank | (uintptr_t)adapter) & 3) == 0 && (uintptr_t)y % (out == MOE_F32 ? 4 : 2) == 0 &&
+                  (uintptr_t)base % (base_dtype == MOE_F32 ? 4 : 2) == 0,
+              MOE_EINVAL, "%s: scale, rank, adapter, y and base must be aligned to their elements", fn);
     MOE_CHECK(base != y || (base_dtype == out && ldb == ldy), MOE_EINVAL, "%s: y may be base only with its type and stride", fn);
     MOE_CHECK(ws_bytes >= moe_lora_workspace_bytes(M, r), MOE_ENOMEM, "%s: workspace of %zu bytes, need %zu", fn, ws_bytes,
               moe_lora_workspace_bytes(M, r));

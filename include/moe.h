@@ -259,7 +259,8 @@ MOE_API moe_status moe_combine(const void* y_perm, moe_dtype y_dtype, const floa
  *   rounded once.  h is rounded to bf16 when act is BF16 (quantised with FP8_B128 weights, as x is), every
  *   sum is binary32, gates are applied to binary32 sums; the order of the sums is this call's own, so y
  *   differs from the separate calls' by the roundings that fall otherwise.  It is the same for the
- *   same inputs, and a token's row does not depend on the other tokens of the call's values.
+ *   same inputs.  A token's row takes nothing from the other rows' values (not their NaN either); which experts they chose
+ *   decides where its own sum over the experts is cut, so with others its last bits may differ.
  *   An expert in slot MOE_SLOT_ELSEWHERE adds nothing; one in any other slot outside [0, n_slots) neither, and
  *   sets the status word to 1.
  * Types: x, w_router, y act; F32 weights with act F32; BF16, INT4_G128 and FP8_B128 weights with act BF16.

@@ -27,7 +27,8 @@ from expert_offload_cache_amd import build as b  # noqa: E402
 
 OUT_DIR = os.path.join(ROOT, "_build", "asan")
 LIB = os.path.join(OUT_DIR, "libmoe.so")
-TESTS = ["tests/test_cache_host.py", "tests/test_cpu_expert.py", "tests/test_abi.py", "tests/test_fp8_host.py"]
+TESTS = ["tests/test_cache_host.py", "tests/test_cpu_expert.py", "tests/test_abi.py", "tests/test_fp8_host.py",
+         "tests/test_few_lora_host.py"]
 # host-pass only: every sanitizer flag goes through -Xarch_host
 HOST_SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer",
