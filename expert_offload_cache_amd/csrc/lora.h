@@ -23,6 +23,8 @@ struct LoraArgs {
     void* y;                 // [M, N]
     size_t ldy;
     float* v;  // workspace [M, r]
+    float* part;  // workspace [splits, M, N]: sums of x W^T over runs of the inputs
+    int splits;   // 0: launch 2 forms x W^T
     bool wide;  // the rows of y and base start on 16 bytes
 };
 
@@ -36,6 +38,9 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) { return f32_to_bf16(v); }
 
+// runs of the inputs whose sums launch 1 leaves
+constexpr size_t kLoraPartBytes = (size_t)1 << 20;
+int lora_splits(const LoraArgs& p);
 // one row and a low rank: v is formed by the launch that uses it
 bool lora_alone(const LoraArgs& p);
 // v = scale A x for the rows that have an adapter

@@ -128,13 +128,11 @@ __device__ __forceinline__ void stream_steps(int s0, int s1, int K, int q, Row&&
 // ---- launch 1 ---------------------------------------------------------------------------------------
 // A workgroup takes 16 * NM rows and NR blocks of 16 ranks; its NW waves split the inputs, each with the loads of C
 // steps on their way.  Of its rows' adapters it takes every Z-th.
+// red: NW * NM * NR KB of LDS.
 template <int NM, int NR, int NW, int C>
-__global__ __launch_bounds__(64 * NW, 4) void lora_shrink_kernel(LoraArgs p) {
-    __shared__ float red[NW * NM * NR * 256];
+__device__ __forceinline__ void shrink_tile(const LoraArgs& p, int m0, int r0, int z, int Z, float* red) {
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // the first adapters' workgroups start last: beside those few that take a tile's second, not before them
-    const int Z = gridDim.z, z = Z - 1 - (int)blockIdx.z, m0 = blockIdx.x * 16 * NM, r0 = blockIdx.y * 16 * NR;
     // every wave: lane i holds row i's adapter (NM <= 4)
     const int mine = lane < 16 * NM ? adapter_of(p, m0 + lane) : -1;
     uint64_t left = __ballot(mine >= 0);
@@ -172,6 +170,51 @@ __global__ __launch_bounds__(64 * NW, 4) void lora_shrink_kernel(LoraArgs p) {
             if (((rows >> m) & 1) && c < rank) p.v[(size_t)(m0 + m) * p.r + c] = scale * s;
         }
         if (left) __syncthreads();
+    }
+}
+
+template <int NM, int NR, int NW, int C>
+__global__ __launch_bounds__(64 * NW, 4) void lora_shrink_kernel(LoraArgs p) {
+    __shared__ float red[NW * NM * NR * 256];
+    // the first adapters' workgroups start last: beside those few that take a tile's second, not before them
+    shrink_tile<NM, NR, NW, C>(p, blockIdx.x * 16 * NM, blockIdx.y * 16 * NR, gridDim.z - 1 - blockIdx.z, gridDim.z, red);
+}
+
+// A few rows and a narrow matrix: x W^T needs nothing of v, so one launch forms both.  After the workgroups of the form above
+// come those of the product, 16 columns and a run of inputs each (`splits` of them, so that every compute unit
+// has work); launch 2 adds their sums up.
+constexpr int kBothWaves = 8;
+
+template <int MB>
+__global__ __launch_bounds__(64 * kBothWaves, 4) void lora_both_kernel(LoraArgs p, int rank_blocks, int Z) {
+    constexpr int NW = kBothWaves;
+    __shared__ float red[NW * MB * 256];
+    const int tiles = (p.M + 15) / 16, shrink = tiles * rank_blocks * Z;
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int id = blockIdx.x;
+    if (id < shrink) {
+        shrink_tile<1, 1, NW, 8>(p, id % tiles * 16, id / tiles % rank_blocks * 16, id / (tiles * rank_blocks), Z, red);
+        return;
+    }
+    id -= shrink;
+    const int cols = (p.N + 15) / 16, n0 = id % cols * 16, split = id / cols, nst = (p.K + 31) / 32;
+    const int s0 = (int)((int64_t)split * nst / p.splits), n = (int)((int64_t)(split + 1) * nst / p.splits) - s0;
+    f32x4_t acc[1][MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) acc[0][i] = zerof();
+    stream_steps<MB, 1, 8, MB <= 3 ? 4 : 2>(s0 + wv * n / NW, s0 + (wv + 1) * n / NW, p.K, q,
+        [&](int) __attribute__((always_inline)) { return p.w + (size_t)min(n0 + r16, p.N - 1) * p.ldw; },
+        [&](int i) __attribute__((always_inline)) { return p.x + (size_t)min(16 * i + r16, p.M - 1) * p.ldx; }, acc);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) *(f32x4_t*)&red[(wv * MB + i) * 256 + r16 * 16 + 4 * q] = acc[0][i];
+    __syncthreads();
+    for (int o = tid; o < p.M * 16; o += 64 * NW) {
+        if (n0 + (o & 15) >= p.N) continue;
+        float s = red[o];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) s += red[w * MB * 256 + o];
+        p.part[((size_t)split * p.M + (o >> 4)) * p.N + n0 + (o & 15)] = s;
     }
 }
 
@@ -278,7 +321,16 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
     const int n0 = blockIdx.x * 16, nst = (p.K + 31) / 32;
     const int only = kAlone ? __builtin_amdgcn_readfirstlane(adapter_of(p, 0)) : -1;
     auto x_row = [&](int i) __attribute__((always_inline)) { return p.x + (size_t)min(16 * i + r16, p.M - 1) * p.ldx; };
-    if (wv < H && p.w) {
+    const bool product = p.w && !p.splits;
+    // (a thread has one element of the result at most)
+    const int row = tid >> 4, col = n0 + (tid & 15);
+    const bool mine = row < p.M && col < p.N;
+    float sum0 = 0.f, base = 0.f;
+    if (mine) {
+        for (int i = 0; i < p.splits; ++i) sum0 += p.part[((size_t)i * p.M + row) * p.N + col];
+        if (p.base) base = to_f32(((const BaseT*)p.base)[(size_t)row * p.ldb + col]);
+    }
+    if (wv < H && product) {
         f32x4_t acc[1][MB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) acc[0][i] = zerof();
@@ -309,7 +361,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
     }
     // rows first, first + step, ...: lane l takes column l / 4 and inputs 8 (l % 4) .. + 7 of each 32
     constexpr int F = MB >= 3 ? 4 : MB;  // rows whose operands are read together
-    const int first = p.w && !kAlone ? wv - H : wv, step = p.w && !kAlone ? H : kStreamWaves;
+    const int first = product && !kAlone ? wv - H : wv, step = product && !kAlone ? H : kStreamWaves;
     const int n = min(n0 + (lane >> 2), p.N - 1);
     for (int m0 = first; m0 >= 0 && m0 < p.M; m0 += step * F) {
         int ad[F], rank[F];
@@ -355,18 +407,13 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
         }
     }
     __syncthreads();
-    for (int o = tid; o < p.M * 16; o += 64 * kStreamWaves) {
-        const int m = o >> 4, c = n0 + (o & 15);
-        float s = 0.f;
-        if (p.w) {
-            s = red[0][o];
+    if (mine) {
+        if (product) {
+            sum0 = red[0][tid];
 #pragma unroll
-            for (int w = 1; w < H; ++w) s += red[w][o];
+            for (int w = 1; w < H; ++w) sum0 += red[w][tid];
         }
-        if (c < p.N) {
-            if (p.base) s += to_f32(((const BaseT*)p.base)[(size_t)m * p.ldb + c]);
-            ((OutT*)p.y)[(size_t)m * p.ldy + c] = from_f32<OutT>(s + delta[o]);
-        }
+        ((OutT*)p.y)[(size_t)row * p.ldy + col] = from_f32<OutT>(sum0 + base + delta[tid]);
     }
 }
 
@@ -675,13 +722,25 @@ moe_status launch_rows(const LoraArgs& p, moe_dtype base, hipStream_t st) {
 
 }  // namespace
 
+int lora_splits(const LoraArgs& p) {
+    if (!p.w || p.M > kStreamRows || lora_alone(p)) return 0;
+    const int splits = std::min(std::max(256 / ((p.N + 15) / 16), 1), (p.K + 511) / 512);
+    return (int)std::min<size_t>(splits, kLoraPartBytes / ((size_t)p.M * p.N * 4));
+}
+
 bool lora_alone(const LoraArgs& p) { return p.M == 1 && p.r <= 32; }
 
 moe_status lora_shrink(const LoraArgs& p, hipStream_t st) {
     if (lora_alone(p)) return MOE_OK;
-    ProfScope ps("lora_shrink", st);
-    const int blocks = (p.M + 15) / 16 * ((p.r + 15) / 16);
-    if (p.M <= kStreamRows) launch_shrink<1, 1, 16, 4>(p, std::min(std::min(p.M, 16), p.n), st);
+    ProfScope ps(p.splits ? "lora_both" : "lora_shrink", st);
+    const int blocks = (p.M + 15) / 16 * ((p.r + 15) / 16), few = std::min(std::min(p.M, 16), p.n);
+    if (p.splits) {
+        const unsigned grid = (unsigned)(blocks * few + (p.N + 15) / 16 * p.splits);
+        if (p.M <= 16) lora_both_kernel<1><<<grid, 64 * kBothWaves, 0, st>>>(p, (p.r + 15) / 16, few);
+        else if (p.M <= 32) lora_both_kernel<2><<<grid, 64 * kBothWaves, 0, st>>>(p, (p.r + 15) / 16, few);
+        else if (p.M <= 48) lora_both_kernel<3><<<grid, 64 * kBothWaves, 0, st>>>(p, (p.r + 15) / 16, few);
+        else lora_both_kernel<4><<<grid, 64 * kBothWaves, 0, st>>>(p, (p.r + 15) / 16, few);
+    } else if (p.M <= kStreamRows) launch_shrink<1, 1, 16, 4>(p, few, st);
     else if (blocks < 256) launch_shrink<1, 1, 16, 4>(p, std::min(p.n, 2), st);
     else launch_shrink<2, 2, 8, 4>(p, std::min(p.n, 2), st);
     return check_launch("lora_shrink");

@@ -7,7 +7,7 @@ extern "C" {
 
 size_t moe_lora_workspace_bytes(int M, int r) {
     if (M < 0 || r < 8 || r > MOE_LORA_MAX_RANK || r % 8 != 0) return 0;
-    return align_up((size_t)M * r * 4, 256) + 256;
+    return align_up((size_t)M * r * 4, 256) + kLoraPartBytes;
 }
 
 moe_status moe_lora_linear(const void* x, size_t ldx, int M, int K, const void* w, size_t ldw, int N, const void* base,
@@ -37,7 +37,8 @@ moe_status moe_lora_linear(const void* x, size_t ldx, int M, int K, const void* 
     MOE_CHECK(ws_bytes >= moe_lora_workspace_bytes(M, r), MOE_ENOMEM, "%s: workspace of %zu bytes, need %zu", fn, ws_bytes,
               moe_lora_workspace_bytes(M, r));
     LoraArgs p{(const uint16_t*)x, ldx, M, K, (const uint16_t*)w, ldw, N, base, ldb, (const uint16_t*)a, (const uint16_t*)b, r, n,
-               scale, rank, adapter, y, ldy, (float*)ws, false};
+               scale, rank, adapter, y, ldy, (float*)ws, (float*)((uint8_t*)ws + align_up((size_t)M * r * 4, 256)), 0, false};
+    p.splits = lora_splits(p);
     auto starts_wide = [](const void* q, size_t ld, moe_dtype t) { return (((uintptr_t)q | ld * (t == MOE_F32 ? 4 : 2)) & 15) == 0; };
     p.wide = starts_wide(y, ldy, out) && (!base || starts_wide(base, ldb, base_dtype));
     hipStream_t st = (hipStream_t)s;
