@@ -2,8 +2,8 @@
 //
 //   y[m,:] = x[m,:] W^T + base[m,:] + scale_a (x[m,:] A_a^T) B_a^T,   a = adapter[m]
 //
-// Launch 1 (lora_shrink_kernel): v[m,:] = scale_a A_a x[m,:] for the rows that have an adapter, in binary32.
-// Launch 2: the projection, with the adapters' second product at its end.
+// Launch 1: v[m,:] = scale_a A_a x[m,:] for the rows that have an adapter, in binary32 (for few rows also the sums of
+// x W^T over runs of the inputs).  Launch 2: the projection, with the adapters' second product at its end.
 //
 // v is binary32 and the matrix instructions take bf16, so v enters as a sum of bf16 parts: v1 = bf16(v),
 // v2 = bf16(v - v1), v3 = bf16(v - v1 - v2); two parts hold 16 bits of it, which is beyond what a bf16
