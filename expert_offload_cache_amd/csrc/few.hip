@@ -21,14 +21,22 @@
 // launch.  Launch 1 fills h with a mark (all bits set, which is a NaN that h never holds: a NaN
 // result of those bits is stored as another NaN).  h is written and read with device-scope accesses of
 // whole words, and a reader that finds the mark reads again: each word is its own flag.
-// Why every wait ends: items are handed out by counters, gate/up items first, and gate/up items wait for
-// nothing.  A workgroup gets a down item only after all gate/up items have been handed out to workgroups that
-// run already, whatever else occupies the device.  (A second call that uses the same workspace
-// at the same time breaks this; then the wait ends at its limit and the status word is set to 2.)
+// Why every wait ends.  There are two: for h, and of the workgroup of run 0 of a row block for the other runs' sums
+// of y (store_y).  Items are handed out by counters to workgroups that run, each when it asks; nobody waits for an item
+// that is not handed out:
+//  - Gate/up items wait for nothing, and a workgroup gets a down item only after all of them have been handed out.  So
+//    every wait for h ends.
+//  - The runs of a row block lie in one list, run 0 last (few_order.h), so run 0 waits for items handed out before it.  A
+//    workgroup asks for its next item before it has finished the one at hand, so an item may be held by a workgroup that
+//    waits first: then with a run 0 that was handed out to it before the item.  Whoever follows such a chain of waits
+//    goes back in the order of hand-out at each step, so the chain closes no circle and ends with somebody who works.
+// Neither needs all workgroups to be resident, nor any order among those that are.  (A second call that uses the same
+// workspace at the same time breaks both; then a wait ends at its limit and the status word is set to 2.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
+#include "few_order.h"
 #include "ffn_common.h"
 #include "fp8.h"
 #include "route_logit.h"
@@ -41,10 +49,8 @@ namespace {
 constexpr int kFewTok = MOE_FEW_TOKENS;    // most tokens: one operand block of the matrix instructions
 constexpr int kFewK = MOE_FEW_TOPK;        // most experts a token
 constexpr int kFewRows = kFewTok * kFewK;  // most (token, expert) pairs
-constexpr int kWaves = 8;                  // of a workgroup of launch 2
+constexpr int kWaves = kFewWaves;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kUnits = 256;                // compute units: launch 2 has a workgroup for each
-constexpr int kLists = 8;                  // counters of each kind, a cache line each: one word takes 11 ns an increment
 constexpr int kListStride = 64;            // words from a counter to the next
 constexpr uint32_t kMark = 0xFFFFFFFFu;    // a word of h that is not written yet
 constexpr int kEarlyGates = 4;             // most tokens whose gates are formed before the first products
@@ -444,24 +450,23 @@ __device__ __forceinline__ void few_gates(const FewArgs& a, FewTable& tb, Choice
     __syncthreads();
 }
 
-// The next work item of a kind (one wave): item c + kLists v is the v-th of list c.  A workgroup
-// starts with the list of its number and goes on to the others; -1: every list is handed out.
+// The next work item of a kind (one wave): item c + kLists v is the v-th of list c (few_order.h: `total` things, `runs`
+// items each).  A workgroup starts with the list of its number and goes on to the others; -1: every list is handed out.
 __device__ __forceinline__ uint32_t few_request(uint32_t* lists, int c) {
     uint32_t v = 0;
     if ((threadIdx.x & 63) == 0) v = __hip_atomic_fetch_add(lists + c * kListStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return v;  // lane 0's
 }
-__device__ __forceinline__ int few_resolve(uint32_t* lists, int total, int home, uint32_t asked) {
+__device__ __forceinline__ int few_resolve(uint32_t* lists, int total, int runs, int home, uint32_t asked) {
     const int lane = threadIdx.x & 63;
     int c = home;
     for (;;) {
         const uint32_t v = __builtin_amdgcn_readfirstlane(asked);
-        const int n = (total - c + kLists - 1) / kLists;
-        if ((int)v < n) return c + kLists * (int)v;
+        if ((int)v < list_items(total, runs, c)) return c + kLists * (int)v;
         // another list that is not handed out yet
         const int o = (home + lane) % kLists;
         const uint32_t seen = lane < kLists ? __hip_atomic_load(lists + o * kListStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-        const uint64_t left = __ballot(lane < kLists && (int)seen < (total - o + kLists - 1) / kLists);
+        const uint64_t left = __ballot(lane < kLists && (int)seen < list_items(total, runs, o));
         if (!left) return -1;
         c = (home + __builtin_ctzll(left)) % kLists;
         asked = few_request(lists, c);
@@ -730,11 +735,11 @@ struct Down {
 #pragma unroll
         for (int r = FROM; r < TO; ++r) load_w(r);
     }
-    __device__ __forceinline__ void begin(int b, int split) {
+    __device__ __forceinline__ void begin(DownItem it) {
         const int64_t all = (int64_t)tb.n_items * nch;
-        c0 = (int)(split * all / a.splits);
-        c1 = (int)((split + 1) * all / a.splits);
-        block_at = down_block_offset(b * RB, a.d, a.f, (moe_dtype)W);
+        c0 = (int)(it.run * all / a.splits);
+        c1 = (int)((it.run + 1) * all / a.splits);
+        block_at = down_block_offset(it.block * RB, a.d, a.f, (moe_dtype)W);
 #pragma unroll
         for (int m = 0; m < RB; ++m) y[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         begin_batch(c0);
@@ -883,7 +888,7 @@ struct Down {
 
 // The waves' sums of a down item joined: the first run's workgroup adds the others' and stores y.
 template <int RB>
-__device__ __forceinline__ void store_y(const FewArgs& a, bool wide, int b, int split, const float* red, bool& lost) {
+__device__ __forceinline__ void store_y(const FewArgs& a, bool wide, DownItem it, const float* red, bool& lost) {
     const int lane = threadIdx.x & 63;
     const size_t part = (size_t)a.T * a.d;
     for (int o = threadIdx.x; o < a.T * 16 * RB; o += kThreads) {  // whole waves
@@ -891,11 +896,11 @@ __device__ __forceinline__ void store_y(const FewArgs& a, bool wide, int b, int 
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) s += red[w * 256 * RB + o];
-        const size_t at = (size_t)t * a.d + b * 16 * RB + r;
-        if (split > 0) {
+        const size_t at = (size_t)t * a.d + it.block * 16 * RB + r;
+        if (it.run > 0) {
             uint32_t v = as_u32(s);
             if (v == kMark) v = 0x7FFFFFFFu;
-            __hip_atomic_store(a.part + (split - 1) * part + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(a.part + (it.run - 1) * part + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             continue;
         }
         for (int p = 1; p < a.splits; p += 4) {
@@ -942,9 +947,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     if (asks) ask0 = few_request(gu_lists, home);
     int gate_up = 0;
     auto resolve = [&](uint32_t asked) __attribute__((always_inline)) {
-        int it = few_resolve(gu_lists, gate_up, home, asked);
+        int it = few_resolve(gu_lists, gate_up, 1, home, asked);
         if (it < 0) {
-            it = few_resolve(dn_lists, db * a.splits, home, few_request(dn_lists, home));
+            it = few_resolve(dn_lists, db, a.splits, home, few_request(dn_lists, home));
             if (it >= 0) it += gate_up;
         }
         if (lane == 0) tb.next = it;
@@ -965,8 +970,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         return;
     }
     auto is_gu = [&](int it) __attribute__((always_inline)) { return it >= 0 && it < gate_up; };
-    // the first run of a row block, which adds the others, is handed out last
-    auto split_of = [&](int it) __attribute__((always_inline)) { return a.splits - 1 - (it - gate_up) / db; };
+    auto down_of = [&](int it) __attribute__((always_inline)) { return down_item(it - gate_up, db, a.splits); };
     int it = __builtin_amdgcn_readfirstlane(tb.next);
     bool lost = false;
     Down<W, RB, CD, RD, RE> dn(a, tb);
@@ -1009,7 +1013,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         }
         // the first down item's weights before the last gate/up item's products
         if (next >= 0) {
-            dn.begin((next - gate_up) % db, split_of(next));
+            dn.begin(down_of(next));
             dn.template load<0, RE>();
         }
         if (works) {
@@ -1027,7 +1031,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     __syncthreads();
     while (it >= 0) {
         if (ask && asks) {
-            const int next = few_resolve(dn_lists, db * a.splits, home, few_request(dn_lists, home));
+            const int next = few_resolve(dn_lists, db, a.splits, home, few_request(dn_lists, home));
             if (lane == 0) tb.next = next < 0 ? -1 : next + gate_up;
         }
         ask = false;
@@ -1044,12 +1048,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
                 for (int i = 0; i < 4; ++i)
                     red[wv * 256 * RB + acc_token<W>(lane, i) * 16 * RB + 16 * m + acc_row<W>(lane, i)] = dn.y[m][i];
             __syncthreads();
-            store_y<RB>(a, W == MOE_F32, (it - gate_up) % db, split_of(it), red, lost);
+            store_y<RB>(a, W == MOE_F32, down_of(it), red, lost);
             it = __builtin_amdgcn_readfirstlane(tb.next);
             ask = true;
             __syncthreads();  // red and the number have been read
             if (it < 0) break;
-            dn.begin((it - gate_up) % db, split_of(it));
+            dn.begin(down_of(it));
         }
         dn.template load<0, RD>();
     }
@@ -1059,21 +1063,6 @@ struct FewLayout {  // workspace: status at byte 0, then
     size_t lists, logits, xq, xs, h, part, total;
     int splits;
 };
-// Columns of y of a down item, in blocks of 16: one where the call's rows of h are few (every unit takes in all of
-// them), four elsewhere.
-int few_row_blocks(int T, int f, int k, bool shared, moe_dtype w) {
-    const size_t rows = (size_t)T * k + (shared ? T : 0);
-    return rows * f * (w == MOE_F32 ? 4 : 2) <= ((size_t)48 << 10) ? 1 : 4;
-}
-// Runs of the down items' pairs: as many as give every one of 256 workgroups an item, while a wave has two steps
-// and more.
-int few_splits(int T, int d, int f, int E, int k, bool shared, moe_dtype w) {
-    const int items = std::min(T * k, E) + (shared ? 1 : 0), rb = few_row_blocks(T, f, k, shared, w);
-    const int64_t steps = (int64_t)items * (f / (w == MOE_F32 || w == MOE_BF16 ? 32 : 128));
-    int s = 1;
-    while (s < 16 && 2 * s * (d / (16 * rb)) <= kUnits && steps >= (int64_t)2 * s * kWaves * 2) s *= 2;
-    return s;
-}
 FewLayout few_layout(int T, int d, int f, int E, int k, bool shared, moe_dtype w) {
     FewLayout l;
     const size_t rows = (size_t)T * k + (shared ? T : 0), esz = w == MOE_F32 || w == MOE_FP8_B128 ? 4 : 2;
@@ -1119,7 +1108,7 @@ moe_status launch_shape(FewArgs a, hipStream_t st) {
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
     // a workgroup a compute unit, fewer where there are fewer items
     const int64_t items = (int64_t)a.items_most * (a.f / 16 / PB) + a.d / 16 / RB * a.splits;
-    kern<<<(unsigned)std::min<int64_t>(kUnits, items), kThreads, lds, st>>>(a);
+    kern<<<(unsigned)std::min<int64_t>(kFewUnits, items), kThreads, lds, st>>>(a);
     return MOE_OK;
 }
 
