@@ -66,6 +66,28 @@ def _s(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _new(stream, device, *specs, zero=False):
+    """Tensors (shape, dtype) that a call makes for itself, uninitialised or zero-filled, on the stream that it launches on: a
+    fill comes before the kernels, and the memory is neither in use by earlier work of the current stream nor given back to
+    it while the kernels run.  On another stream than the current one they are marked as used by that one too: the caller
+    may drop a result while its work there (after the launch stream's) is pending."""
+    torch = _torch()
+    make = torch.zeros if zero else torch.empty
+    handle = None if stream is None else _s(stream)
+    if handle is None or handle == _s(None):
+        return [make(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    if handle == 0:
+        side = torch.cuda.default_stream(device)
+    else:
+        side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
+    user = torch.cuda.current_stream(device)
+    with torch.cuda.stream(side):
+        ts = [make(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    for t in ts:
+        t.record_stream(user)
+    return ts
+
+
 def _contig(*ts):
     for t in ts:
         if t is not None and not t.is_contiguous():
@@ -404,16 +426,15 @@ def layer_few(x, w_router, bias, k: int, slot_of_expert, slot_pool, n_slots: int
               shared_w=None, forced_idx=None, out=None, ws=None, stream=None):
     """The whole layer for at most 16 tokens (moe_layer_few): route, experts and combine in two launches.
     x [T, d], w_router [E, d] of x's type; bias f32 [E] or None; slots as expert_ffn_grouped takes them.
-    out: (y, topk_idx, topk_w) to write into; ws: layer_few_workspace_bytes, zero-filled before its first use
-    and used by one call at a time.  -> (y [T, d], topk_idx int32 [T, k], topk_w f32 [T, k])."""
+    out: (y, topk_idx, topk_w) to write into; ws: layer_few_workspace_bytes, zero-filled before its first use (on
+    `stream`, or ordered before it) and used by one call at a time.  -> (y [T, d], topk_idx int32 [T, k], topk_w f32 [T, k])."""
     torch = _torch()
     act = _act(x)
     T, d = x.shape
     E = w_router.shape[0]
     dt, f32, i32 = x.dtype, torch.float32, torch.int32
     if out is None:
-        out = (torch.empty((T, d), dtype=dt, device=x.device), torch.empty((T, k), dtype=i32, device=x.device),
-               torch.empty((T, k), dtype=f32, device=x.device))
+        out = tuple(_new(stream, x.device, ((T, d), dt), ((T, k), i32), ((T, k), f32)))
     y, idx, w = out
     for name, t, shape, dtype in (("x", x, (T, d), dt), ("w_router", w_router, (E, d), dt), ("y", y, (T, d), dt),
                                   ("topk_idx", idx, (T, k), i32), ("topk_w", w, (T, k), f32)):
@@ -432,8 +453,8 @@ def layer_few(x, w_router, bias, k: int, slot_of_expert, slot_pool, n_slots: int
     if slot_pool.nbytes < (n_slots - 1) * slot_stride + slot:
         raise ValueError(f"slot_pool must hold {n_slots} slots of {slot_stride} bytes, got {slot_pool.nbytes} bytes")
     if ws is None:
-        ws = torch.zeros(layer_few_workspace_bytes(T, d, f, E, k, shared_w is not None, wdt) or 1, dtype=torch.uint8,
-                         device=x.device)
+        need = layer_few_workspace_bytes(T, d, f, E, k, shared_w is not None, wdt) or 1
+        ws, = _new(stream, x.device, (need, torch.uint8), zero=True)
     _on_current_device(x, w_router, bias, forced_idx, slot_of_expert, slot_pool, shared_w, y, idx, w, ws)
     check(lib().moe_layer_few(_p(x), act, T, d, f, E, k, _p(w_router), _p(bias), _p(forced_idx), _p(slot_of_expert),
                               n_slots, _p(slot_pool), slot_stride, WDT[wdt], _p(shared_w), _p(idx), _p(w), _p(y),

@@ -108,7 +108,8 @@ class DeviceLayer:
             ws=self.workspace(T), pws=permute_workspace(T, k, E, dev))
 
     def buffers_few(self, T: int):
-        """Outputs and workspace of a T-token forward_few (at most 16), allocated once."""
+        """Outputs and workspace of a T-token forward_few (at most 16), allocated once, on the current stream: a call
+        on another stream comes after it."""
         import torch
 
         act = torch.bfloat16 if self.act == "bf16" else torch.float32
