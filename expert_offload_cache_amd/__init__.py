@@ -354,7 +354,7 @@ def lora_linear(x, a, b, scale, adapter, w=None, base=None, rank=None, out=None,
     N = b.shape[1]
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or bf16, device=x.device)
+        out, = _new(stream, x.device, ((M, N), out_dtype or bf16))
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
     for name, t in (("the result", out), ("base", base)):
@@ -370,7 +370,7 @@ def lora_linear(x, a, b, scale, adapter, w=None, base=None, rank=None, out=None,
     if rank is not None:
         _dense("rank", rank, (n,), i32)
     if ws is None:
-        ws = torch.empty(lora_workspace_bytes(M, r) or 1, dtype=torch.uint8, device=x.device)
+        ws, = _new(stream, x.device, (lora_workspace_bytes(M, r) or 1, torch.uint8))
     else:
         _contig(ws)
     _on_current_device(x, a, b, scale, adapter, w, base, rank, out, ws)

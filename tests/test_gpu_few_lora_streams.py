@@ -4,6 +4,7 @@ import pytest
 
 from gpu_util import need_gpu
 from test_gpu_few import make as make_layer
+from test_gpu_lora import make as make_lora
 
 pytestmark = pytest.mark.gpu
 
@@ -88,6 +89,34 @@ def test_layer_few_makes_its_workspace_on_the_launch_stream(wdt, T, monkeypatch)
         assert busy_still, "the current stream was to be busy while the other one ran"
         for g, w in zip(got, want):
             assert torch.equal(g.cpu(), w.cpu())
+        monkeypatch.undo()
+        torch.cuda.synchronize()
+        del a
+
+
+@pytest.mark.parametrize("M,w,base", [(1, True, None), (20, True, "bf16"), (64, False, "f32"), (200, True, None), (300, False, "bf16")])
+def test_lora_linear_makes_its_workspace_on_the_launch_stream(M, w, base, monkeypatch):
+    need_gpu()
+    import torch
+
+    import expert_offload_cache_amd as moe
+
+    s, dt = make_lora(M, 264, 512, 32, 4, w=w, base=base, seed=M)
+    want = moe.lora_linear(**s).cpu()
+    need = moe.lora_workspace_bytes(M, 32)
+    side, forms = streams()
+    seen = Watched(moe.lib(), "moe_lora_linear")
+    for name, st in forms:
+        soiled([need])
+        monkeypatch.setattr(moe, "lib", lambda: seen)
+        print(f"lora_linear on {name}, M={M} w={w} base={base}", flush=True)
+        a = busy()
+        got = moe.lora_linear(**s, stream=st)
+        assert kept_from(seen.given[-1][-3], need)
+        busy_still = not torch.cuda.current_stream().query()
+        side.synchronize()
+        assert busy_still, "the current stream was to be busy while the other one ran"
+        assert torch.equal(got.cpu(), want)
         monkeypatch.undo()
         torch.cuda.synchronize()
         del a
