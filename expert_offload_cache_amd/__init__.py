@@ -104,9 +104,8 @@ def route(x, w_router, bias, k: int, forced_idx=None, out=None, stream=None):
     T, d = x.shape
     E = w_router.shape[0]
     if out is None:
-        out = (torch.empty((T, k), dtype=torch.int32, device=x.device),
-               torch.empty((T, k), dtype=torch.float32, device=x.device),
-               torch.empty((T, E), dtype=torch.float32, device=x.device))
+        f32 = torch.float32
+        out = tuple(_new(stream, x.device, ((T, k), torch.int32), ((T, k), f32), ((T, E), f32)))
     idx, w, logits = out
     check(lib().moe_route(_p(x), _act(x), T, d, _p(w_router), _p(bias), E, k, _p(forced_idx), _p(idx), _p(w),
                           _p(logits), _s(stream)))
@@ -117,10 +116,10 @@ def permute_workspace_bytes(T: int, k: int, E: int) -> int:
     return int(lib().moe_permute_workspace_bytes(T, k, E))
 
 
-def permute_workspace(T: int, k: int, E: int, device):
-    """Device scratch for a split sort of T*k pairs (None when one workgroup sorts)."""
+def permute_workspace(T: int, k: int, E: int, device, stream=None):
+    """Device scratch for a split sort of T*k pairs (None when one workgroup sorts), made on `stream`."""
     n = permute_workspace_bytes(T, k, E)
-    return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
+    return _new(stream, device, (n, _torch().uint8))[0] if n else None
 
 
 def permute(topk_idx, E: int, out=None, stream=None, ws=None):
@@ -129,9 +128,8 @@ def permute(topk_idx, E: int, out=None, stream=None, ws=None):
     _contig(topk_idx)
     T, k = topk_idx.shape
     if out is None:
-        dev = topk_idx.device
-        out = (torch.empty(E, dtype=torch.int32, device=dev), torch.empty(E + 1, dtype=torch.int32, device=dev),
-               torch.empty(T * k, dtype=torch.int32, device=dev), torch.empty(T * k, dtype=torch.int32, device=dev))
+        i32 = torch.int32
+        out = tuple(_new(stream, topk_idx.device, (E, i32), (E + 1, i32), (T * k, i32), (T * k, i32)))
     c, o, p, ip = out
     check(lib().moe_permute(_p(topk_idx), T, k, E, _p(c), _p(o), _p(p), _p(ip), _p(ws),
                             0 if ws is None else ws.numel(), _s(stream)))
@@ -146,11 +144,9 @@ def route_permute(x, w_router, bias, k: int, forced_idx=None, out=None, stream=N
     T, d = x.shape
     E = w_router.shape[0]
     if out is None:
-        dev = x.device
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
-               torch.empty((T, E), dtype=torch.float32, device=dev), torch.empty(E, dtype=torch.int32, device=dev),
-               torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(T * k, dtype=torch.int32, device=dev),
-               torch.empty(T * k, dtype=torch.int32, device=dev))
+        i32, f32 = torch.int32, torch.float32
+        out = tuple(_new(stream, x.device, ((T, k), i32), ((T, k), f32), ((T, E), f32), (E, i32), (E + 1, i32), (T * k, i32),
+                         (T * k, i32)))
     idx, w, logits, c, o, p, ip = out
     check(lib().moe_route_permute(_p(x), _act(x), T, d, _p(w_router), _p(bias), E, k, _p(forced_idx), _p(idx),
                                   _p(w), _p(logits), _p(c), _p(o), _p(p), _p(ip), _p(ws),
@@ -197,12 +193,12 @@ def expert_ffn_grouped(x, perm, offsets, counts, slot_of_expert, slot_pool, n_sl
     act = _act(x)
     rows = T * k + (T if shared_w is not None else 0)
     if y_perm is None:
-        y_perm = torch.empty((rows, d), dtype=y_dtype or torch.float32, device=x.device)
+        y_perm, = _new(stream, x.device, ((rows, d), y_dtype or torch.float32))
     _expert_tensors(T, d, f, E, k, wdt, perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
                     y_perm)
     if ws is None:
         need = workspace_bytes(T, d, f, E, k, shared_w is not None, act, WDT[wdt])
-        ws = torch.zeros(need, dtype=torch.uint8, device=x.device)
+        ws, = _new(stream, x.device, (need, torch.uint8), zero=True)
     check(lib().moe_expert_ffn_grouped(_p(x), act, T, d, f, E, k, _p(perm), _p(offsets), _p(counts),
                                        _p(slot_of_expert), n_slots, _p(slot_pool), slot_stride, WDT[wdt],
                                        _p(shared_w), _p(y_perm), _y_code(y_perm), _p(ws), ws.numel(), _s(stream)))
@@ -253,13 +249,12 @@ def _dense(name, t, shape, dtype) -> None:
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-def _quantised_out(x, shape, q, scale):
+def _quantised_out(x, shape, q, scale, stream):
     """The given (or new) e4m3 rows and scales of `shape` -> (q, scale, elements from a row of q to the next)."""
     torch = _torch()
     groups = (shape[0], (shape[1] + 127) // 128)
     if q is None and scale is None:
-        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scale = torch.empty(groups, dtype=torch.float32, device=x.device)
+        q, scale = _new(stream, x.device, (shape, torch.float8_e4m3fn), (groups, torch.float32))
     elif q is None or scale is None:
         raise ValueError("q and scale come together")
     ldq = _rows("q", q, shape, torch.float8_e4m3fn)
@@ -279,8 +274,8 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, emit: str = "y", ou
     if emit not in ("y", "fp8", "both"):
         raise ValueError(f'emit must be "y", "fp8" or "both", got {emit!r}')
     if out is None:
-        y = torch.empty(shape, dtype=dt, device=x.device) if emit != "fp8" else None
-        h = torch.empty(shape, dtype=dt, device=x.device) if residual is not None else None
+        y = _new(stream, x.device, (shape, dt))[0] if emit != "fp8" else None
+        h = _new(stream, x.device, (shape, dt))[0] if residual is not None else None
         q = scale = None
     else:
         y, h, q, scale = out
@@ -296,7 +291,7 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, emit: str = "y", ou
     if y is not None:
         ldy = _rows("y", y, shape, dt)
     if emit != "y":
-        q, scale, ldq = _quantised_out(x, shape, q, scale)
+        q, scale, ldq = _quantised_out(x, shape, q, scale, stream)
     w_code = act if weight.dtype == dt else MOE_F32
     _dense("weight", weight, (d,), dt if w_code == act else torch.float32)
     _on_current_device(x, weight, residual, y, h, q, scale)
@@ -310,7 +305,7 @@ def quant_fp8(x, out=None, stream=None):
     act = _act(x)
     shape = x.shape
     T, d = shape
-    q, scale, ldq = _quantised_out(x, shape, *(out if out is not None else (None, None)))
+    q, scale, ldq = _quantised_out(x, shape, *(out if out is not None else (None, None)), stream)
     _on_current_device(x, q, scale)
     check(lib().moe_quant_fp8(_p(x), act, T, d, _rows("x", x, shape, x.dtype), _p(q), ldq, _p(scale), _s(stream)))
     return q, scale
@@ -324,7 +319,7 @@ def gemm_fp8(a, a_scale, w, w_scale, out_dtype=None, out=None, stream=None):
     N = w.shape[0]
     G = (K + 127) // 128
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=a.device)
+        out, = _new(stream, a.device, ((M, N), out_dtype or torch.bfloat16))
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
     if out.dtype not in (torch.bfloat16, torch.float32):
@@ -392,10 +387,10 @@ def expert_ffn_fp8(x, x_scale, perm, offsets, counts, slot_of_expert, slot_pool,
     _dense("x_scale", x_scale, (T, (d + 127) // 128), torch.float32)
     rows = T * k + (T if shared_w is not None else 0)
     if y_perm is None:
-        y_perm = torch.empty((rows, d), dtype=y_dtype or torch.float32, device=x.device)
+        y_perm, = _new(stream, x.device, ((rows, d), y_dtype or torch.float32))
     if ws is None:
-        ws = torch.zeros(workspace_bytes(T, d, f, E, k, shared_w is not None, MOE_BF16, MOE_FP8_B128),
-                         dtype=torch.uint8, device=x.device)
+        need = workspace_bytes(T, d, f, E, k, shared_w is not None, MOE_BF16, MOE_FP8_B128)
+        ws, = _new(stream, x.device, (need, torch.uint8), zero=True)
     _expert_tensors(T, d, f, E, k, "fp8", perm, offsets, counts, slot_of_expert, slot_pool, n_slots, slot_stride, shared_w,
                     y_perm)
     _on_current_device(x, x_scale, perm, offsets, counts, slot_of_expert, slot_pool, shared_w, y_perm, ws)
@@ -411,7 +406,7 @@ def combine(y_perm, topk_w, inv_perm, k: int, has_shared: bool, out_dtype, y=Non
     T = topk_w.shape[0]
     d = y_perm.shape[1]
     if y is None:
-        y = torch.empty((T, d), dtype=out_dtype, device=y_perm.device)
+        y, = _new(stream, y_perm.device, ((T, d), out_dtype))
     code = MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32
     check(lib().moe_combine(_p(y_perm), _y_code(y_perm), _p(topk_w), _p(inv_perm), T, k, d, int(bool(has_shared)),
                             _p(y), code, _s(stream)))

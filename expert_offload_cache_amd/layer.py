@@ -8,7 +8,7 @@ from typing import Optional
 
 import numpy as np
 
-from . import (add_rmsnorm, combine, expert_ffn_fp8, expert_ffn_grouped, layer_few, layer_few_workspace_bytes,
+from . import (_new, add_rmsnorm, combine, expert_ffn_fp8, expert_ffn_grouped, layer_few, layer_few_workspace_bytes,
                pack_expert, permute_workspace, route_permute, slot_bytes, workspace_bytes, y_perm_dtype, WDT)
 from ._lib import MOE_BF16, MOE_F32
 
@@ -77,11 +77,11 @@ class DeviceLayer:
     def x_to_device(self, x: np.ndarray):
         return _to_device(x, self.act, self.device)
 
-    def workspace(self, T: int):
+    def workspace(self, T: int, stream=None):
         import torch
 
         n = workspace_bytes(T, self.d, self.f, self.E, self.k, self.shared is not None, self.act_code, WDT[self.wdt])
-        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+        return _new(stream, self.device, (n, torch.uint8), zero=True)[0]
 
     def buffers(self, T: int):
         """Outputs of a T-token forward allocated once (a serving loop's buffers): forward(...,
@@ -158,12 +158,12 @@ class DeviceLayer:
                                                 emit="both" if self.wdt == "fp8" else "y", out=out, stream=stream)
         elif residual is not None:
             raise ValueError("a residual needs a layer with a norm weight")
-        pws = b["pws"] if "pws" in b else permute_workspace(T, self.k, self.E, x.device)
+        pws = b["pws"] if "pws" in b else permute_workspace(T, self.k, self.E, x.device, stream)
         idx, w, logits, counts, offsets, perm, inv = route_permute(x, self.w_router, self.bias, self.k,
                                                                   forced_idx=forced_idx, out=b.get("route"),
                                                                   stream=stream, ws=pws)
         if ws is None:
-            ws = b["ws"] if "ws" in b else self.workspace(T)
+            ws = b["ws"] if "ws" in b else self.workspace(T, stream)
         soe = self.slot_of_expert if slot_of_expert is None else slot_of_expert
         if x8 is not None:
             y_perm, ws = expert_ffn_fp8(x8, x8_scale, perm, offsets, counts, soe, self.pool, self.n_slots, self.stride,

@@ -27,14 +27,12 @@ class Watched:
         return call
 
 
-def busy(ms=30):
-    """Work that keeps the current stream busy for some time."""
+def busy():
+    """Keeps the current stream busy for some time (40 ms or more) and the compute units free: what a call leaves to the current
+    stream comes late (unless the streams happen to share a hardware queue)."""
     import torch
 
-    a = torch.ones(4096, 4096, device="cuda")
-    for _ in range(ms):  # a product of binary32 takes about a millisecond or more
-        a = (a @ a) * 2.0 ** -12
-    return a
+    torch.cuda._sleep(100_000_000)
 
 
 def soiled(sizes):
@@ -55,6 +53,7 @@ def kept_from(address, nbytes, device="cuda"):
 
 
 def streams():
+    """A stream, and the two forms in which a call takes it."""
     import torch
 
     s = torch.cuda.Stream()
@@ -80,18 +79,15 @@ def test_layer_few_makes_its_workspace_on_the_launch_stream(wdt, T, monkeypatch)
         soiled([need])
         monkeypatch.setattr(moe, "lib", lambda: seen)
         print(f"layer_few on {name}, {wdt} T={T}", flush=True)
-        a = busy()
+        busy()
         got = call(stream=s)
         ws = seen.given[-1][-3]  # address, bytes, stream
         assert kept_from(ws, need)
-        busy_still = not torch.cuda.current_stream().query()
         side.synchronize()
-        assert busy_still, "the current stream was to be busy while the other one ran"
         for g, w in zip(got, want):
             assert torch.equal(g.cpu(), w.cpu())
         monkeypatch.undo()
         torch.cuda.synchronize()
-        del a
 
 
 @pytest.mark.parametrize("M,w,base", [(1, True, None), (20, True, "bf16"), (64, False, "f32"), (200, True, None), (300, False, "bf16")])
@@ -110,13 +106,80 @@ def test_lora_linear_makes_its_workspace_on_the_launch_stream(M, w, base, monkey
         soiled([need])
         monkeypatch.setattr(moe, "lib", lambda: seen)
         print(f"lora_linear on {name}, M={M} w={w} base={base}", flush=True)
-        a = busy()
+        busy()
         got = moe.lora_linear(**s, stream=st)
         assert kept_from(seen.given[-1][-3], need)
-        busy_still = not torch.cuda.current_stream().query()
         side.synchronize()
-        assert busy_still, "the current stream was to be busy while the other one ran"
         assert torch.equal(got.cpu(), want)
         monkeypatch.undo()
         torch.cuda.synchronize()
-        del a
+
+
+def separate_calls(moe, layer, x, residual):
+    """The layer's separate calls and those beside them, each with the results and workspaces it makes for itself."""
+    l = layer
+    fp8 = l.wdt == "fp8"
+
+    def run(s):
+        out = {}
+        y, h, q, qs = moe.add_rmsnorm(x, l.norm_weight, residual=residual, emit="both" if fp8 else "y", stream=s)
+        out.update(norm=y, sum=h)
+        rows, rs = moe.quant_fp8(y, stream=s)
+        out.update(rows=rows, rows_scale=rs)
+        out["product"] = moe.gemm_fp8(rows, rs, rows, run.wscale, stream=s)
+        idx, w, logits = moe.route(y, l.w_router, l.bias, l.k, stream=s)
+        counts, offsets, perm, inv = moe.permute(idx, l.E, stream=s)
+        out.update(idx=idx, gate=w, logits=logits, counts=counts, offsets=offsets, perm=perm, inv=inv)
+        if fp8:
+            out["experts"], out["ws"] = moe.expert_ffn_fp8(q, qs, perm, offsets, counts, l.slot_of_expert, l.pool, l.n_slots, l.stride, l.f, l.k,
+                                                            shared_w=l.shared, stream=s)
+        else:
+            out["experts"], out["ws"] = moe.expert_ffn_grouped(y, perm, offsets, counts, l.slot_of_expert, l.pool, l.n_slots, l.stride, l.wdt,
+                                                                l.f, l.k, shared_w=l.shared, stream=s)
+        out["y"] = moe.combine(out["experts"], w, inv, l.k, l.shared is not None, x.dtype, stream=s)
+        return out
+
+    run.wscale = None
+    return run
+
+
+@pytest.mark.parametrize("wdt,T", [("bf16", 3), ("int4", 40), ("fp8", 100)])
+def test_separate_calls_make_their_results_on_the_launch_stream(wdt, T):
+    need_gpu()
+    import numpy as np
+    import torch
+
+    import expert_offload_cache_amd as moe
+    import synth
+    from expert_offload_cache_amd.layer import DeviceLayer
+    from gpu_util import small_workload
+
+    li = synth.layer_inputs(small_workload("bf16", wdt, 256, 128, 10, 3, shared=True), T, seed=T)
+    weight = torch.from_numpy(1 + 0.1 * np.random.default_rng(1).normal(size=256)).bfloat16()
+    layer = DeviceLayer.from_inputs(li, norm_weight=weight.view(torch.int16).numpy().view(np.uint16))
+    x, residual = layer.x_to_device(li.x), torch.randn(T, 256, device="cuda").bfloat16()
+    calls = separate_calls(moe, layer, x, residual)
+    calls.wscale = torch.rand((T + 127) // 128, 2, device="cuda")
+    whole = lambda s: layer.forward(x, residual=residual, stream=s)
+    side, forms = streams()
+    for what, run in (("separate", calls), ("forward", whole)):
+        eager = torch.cuda.Stream()
+        with torch.cuda.stream(eager):
+            run(eager)
+            torch.cuda.synchronize()
+            want = {n: t.clone() for n, t in run(eager).items() if t is not None}
+        torch.cuda.synchronize()
+        sizes = [t.nbytes for t in want.values()]
+        for name, s in forms:
+            soiled(sizes)
+            print(f"{what} on {name}, {wdt} T={T}", flush=True)
+            busy()
+            got = {n: t for n, t in run(s).items() if t is not None}
+            with torch.cuda.stream(side):  # (ordered after the calls, not after the current stream)
+                status = int(got["ws"][:4].view(torch.int32))
+            same = {n: torch.equal(got[n].view(torch.uint8), want[n].view(torch.uint8)) for n in want if n not in ("ws", "residual", "x")}
+            assert all(same.values()) and status == 0, (same, status)
+            places = [(t.data_ptr(), t.nbytes) for t in got.values() if t.data_ptr() not in (x.data_ptr(), residual.data_ptr())]
+            del got
+            assert all(kept_from(*p) for p in places)
+            torch.cuda.synchronize()
