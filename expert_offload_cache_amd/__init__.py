@@ -417,12 +417,28 @@ def layer_few_workspace_bytes(T: int, d: int, f: int, E: int, k: int, has_shared
     return int(lib().moe_layer_few_workspace_bytes(T, d, f, E, k, int(bool(has_shared)), WDT[wdt]))
 
 
+class FewResult(tuple):
+    """(y, topk_idx, topk_w) of layer_few, and the workspace of the call: `status`, its first word, is 0 when every chosen
+    expert was there and every wait ended."""
+
+    ws = None
+
+    @property
+    def status(self):
+        """int32 [1] on the device, written by the call's kernels (sticky in a workspace that is used again)."""
+        torch = _torch()
+        return self.ws.flatten().view(torch.uint8)[:4].view(torch.int32)
+
+
 def layer_few(x, w_router, bias, k: int, slot_of_expert, slot_pool, n_slots: int, slot_stride: int, wdt: str, f: int,
               shared_w=None, forced_idx=None, out=None, ws=None, stream=None):
     """The whole layer for at most 16 tokens (moe_layer_few): route, experts and combine in two launches.
     x [T, d], w_router [E, d] of x's type; bias f32 [E] or None; slots as expert_ffn_grouped takes them.
     out: (y, topk_idx, topk_w) to write into; ws: layer_few_workspace_bytes, zero-filled before its first use (on
-    `stream`, or ordered before it) and used by one call at a time.  -> (y [T, d], topk_idx int32 [T, k], topk_w f32 [T, k])."""
+    `stream`, or ordered before it) and used by one call at a time.
+    -> (y [T, d], topk_idx int32 [T, k], topk_w f32 [T, k]), a tuple whose `.ws` is the workspace and `.status` its status
+    word on the device, to be looked at once the call has run: 1: a chosen expert was in no slot and added nothing; 2: a
+    second call used the workspace at the same time and y is wrong."""
     torch = _torch()
     act = _act(x)
     T, d = x.shape
@@ -454,6 +470,8 @@ def layer_few(x, w_router, bias, k: int, slot_of_expert, slot_pool, n_slots: int
     check(lib().moe_layer_few(_p(x), act, T, d, f, E, k, _p(w_router), _p(bias), _p(forced_idx), _p(slot_of_expert),
                               n_slots, _p(slot_pool), slot_stride, WDT[wdt], _p(shared_w), _p(idx), _p(w), _p(y),
                               _p(ws), ws.nbytes, _s(stream)))
+    out = FewResult(out)
+    out.ws = ws
     return out
 
 

@@ -125,8 +125,9 @@ class DeviceLayer:
 
     def forward_few(self, x, forced_idx=None, stream=None, slot_of_expert=None, bufs=None, residual=None):
         """forward for at most 16 tokens through layer_few: two launches instead of six, no intermediate
-        rows.  Returns a dict with y [T, d], topk_idx, topk_w and, as forward, x and residual.  With `bufs` (from
-        buffers_few(T)) the outputs are written there."""
+        rows.  Returns a dict with y [T, d], topk_idx, topk_w and, as forward, x, residual and ws, whose first 4
+        bytes are the status word (int32, to be looked at: see layer_few).  With `bufs` (from buffers_few(T)) the
+        outputs are written there."""
         b = bufs or {}
         kept = None
         if self.norm_weight is not None:
@@ -137,10 +138,10 @@ class DeviceLayer:
         elif residual is not None:
             raise ValueError("a residual needs a layer with a norm weight")
         soe = self.slot_of_expert if slot_of_expert is None else slot_of_expert
-        y, idx, w = layer_few(x, self.w_router, self.bias, self.k, soe, self.pool, self.n_slots, self.stride, self.wdt,
-                              self.f, shared_w=self.shared, forced_idx=forced_idx, out=b.get("few"), ws=b.get("ws"),
-                              stream=stream)
-        return dict(y=y, topk_idx=idx, topk_w=w, x=x, residual=kept)
+        few = layer_few(x, self.w_router, self.bias, self.k, soe, self.pool, self.n_slots, self.stride, self.wdt, self.f,
+                        shared_w=self.shared, forced_idx=forced_idx, out=b.get("few"), ws=b.get("ws"), stream=stream)
+        y, idx, w = few
+        return dict(y=y, topk_idx=idx, topk_w=w, ws=few.ws, x=x, residual=kept)
 
     def forward(self, x, forced_idx=None, ws=None, stream=None, slot_of_expert=None, bufs=None, residual=None):
         """x: device tensor [T, d].  Returns a dict of every intermediate and y [T, d].  With
