@@ -5,9 +5,11 @@
 // Launch 1: v[m,:] = scale_a A_a x[m,:] for the rows that have an adapter, in binary32 (for few rows also the sums of
 // x W^T over runs of the inputs).  Launch 2: the projection, with the adapters' second product at its end.
 //
-// v is binary32 and the matrix instructions take bf16, so v enters as a sum of bf16 parts: v1 = bf16(v),
-// v2 = bf16(v - v1), v3 = bf16(v - v1 - v2); two parts hold 16 bits of it, which is beyond what a bf16
-// result shows, three all 24.  r is small beside K, so the parts cost little.
+// v is binary32 and the matrix instructions take bf16, so v enters as the sum of kParts = 3 bf16 parts: v1 = bf16(v),
+// v2 = bf16(v - v1), v3 = bf16(v - v1 - v2), 24 bits together.  Two parts hold 16, which is beyond what a bf16 result
+// shows unless the adapters' sum and the rest nearly cancel; then a result from 65 rows on would be worse than one up
+// to 64, where v stays as it is.  The third part takes 1 us of 88 (8192 rows of adapters alone, 4096 wide, rank 64) and
+// 0.4 of 27.5 (1000 x 1001 x 2000, rank 24).
 //
 // Rows of several adapters share a tile: each adapter's product is formed for the whole tile and taken over
 // for its own rows only, by selection, so that an adapter with infinities or NaN touches no other
@@ -230,13 +232,13 @@ __device__ __forceinline__ void load_v(const LoraArgs& p, int m, int k, int rank
 }
 
 // 8 values of v as bf16 parts
-template <int PARTS>
-__device__ __forceinline__ void split_v(const float (&v)[8], u32x4_t (&part)[PARTS]) {
+constexpr int kParts = 3;
+__device__ __forceinline__ void split_v(const float (&v)[8], u32x4_t (&part)[kParts]) {
     float rest[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) rest[i] = v[i];
 #pragma unroll
-    for (int n = 0; n < PARTS; ++n)
+    for (int n = 0; n < kParts; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t w = bf16_pair(rest[2 * i], rest[2 * i + 1]);
@@ -428,8 +430,7 @@ constexpr int kAddCols = 512;
 
 template <typename OutT, typename BaseT>
 __global__ __launch_bounds__(256) void lora_add_kernel(LoraArgs p) {
-    constexpr int PARTS = sizeof(OutT) == 2 ? 2 : 3;
-    __shared__ __align__(16) uint8_t parts[PARTS * 64 * 128];
+    __shared__ __align__(16) uint8_t parts[kParts * 64 * 128];
     __shared__ int s_adapter[64], s_rank[64];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -446,10 +447,10 @@ __global__ __launch_bounds__(256) void lora_add_kernel(LoraArgs p) {
             const int row = i >> 3, c = i & 7, k = k0 + 8 * c;
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (k < s_rank[row]) load_v(p, m0 + row, k, s_rank[row], v);
-            u32x4_t part[PARTS];
-            split_v<PARTS>(v, part);
+            u32x4_t part[kParts];
+            split_v(v, part);
 #pragma unroll
-            for (int n = 0; n < PARTS; ++n) *(u32x4_t*)(parts + (n * 64 + row) * 128 + ((c ^ (row & 7)) << 4)) = part[n];
+            for (int n = 0; n < kParts; ++n) *(u32x4_t*)(parts + (n * 64 + row) * 128 + ((c ^ (row & 7)) << 4)) = part[n];
         }
         __syncthreads();
     };
@@ -499,7 +500,7 @@ __global__ __launch_bounds__(256) void lora_add_kernel(LoraArgs p) {
                     for (int h = 0; h < 2; ++h) {
                         if (k0 + 32 * h >= rank) break;
 #pragma unroll
-                        for (int n = 0; n < PARTS; ++n) {
+                        for (int n = 0; n < kParts; ++n) {
                             const u32x4_t v = *(const u32x4_t*)(parts + (n * 64 + 16 * j + r16) * 128 + (((4 * h + q) ^ (r16 & 7)) << 4));
 #pragma unroll
                             for (int i = 0; i < 4; ++i) d[i] = mfma_bf16(b[i][h], v, d[i]);
@@ -531,17 +532,17 @@ __global__ __launch_bounds__(256) void lora_add_kernel(LoraArgs p) {
 // 16 neighbouring columns of a row, and four lanes' whole lines.
 // 8192 x 4096 x 4096: 260 us (1.06 PFLOP/s), the LDS reads take as long as the products; 1000 x 1001 x 2000: 21 us, latency.
 // The adapters come last: each adapter of the tile's rows, 64 ranks at a time, with B and the parts of v in LDS in the
-// same layout.
+// same layout, multiplied 32 ranks at a time: the registers hold one step's parts beside the tile's sums (both steps'
+// spill at 256 x 256: 308 us a call of 8192 x 4096 x 4096, rank 32, against 288).
 __device__ __forceinline__ int turn_n(int row) { return ((row >> 1) & 1) | ((row >> 4) & 3) << 1; }
 __device__ __forceinline__ int turn_m(int row) { return (row >> 1) & 7; }
 
 template <typename OutT, typename BaseT, int BN, int BM, int WN, int WM, int R>
 __global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) {
     constexpr int NW = WN * WM, RA = BN / WN / 16, CB = BM / WM / 16;
-    constexpr int PARTS = sizeof(OutT) == 2 ? 2 : 3;
     constexpr int kStep = (BN + BM) * 128, kLoads = kStep / 1024 / NW;  // bytes of a step; a wave's 1 KB loads
     static_assert(RA % 4 == 0 && kLoads * NW * 1024 == kStep, "tile shape");
-    static_assert(BN * 128 + PARTS * BM * 128 <= R * kStep, "B and the parts of v fit the ring");
+    static_assert(BN * 128 + kParts * BM * 128 <= R * kStep, "B and the parts of v fit the ring");
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int s_adapter[BM];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r16 = lane & 15;
@@ -633,33 +634,30 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void lora_tile_kernel(LoraArgs p) 
                     const int row = i >> 3, c = i & 7, k = k0 + 8 * c;
                     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     if (k < rank && s_adapter[row] == a) load_v(p, m0 + row, k, rank, v);
-                    u32x4_t part[PARTS];
-                    split_v<PARTS>(v, part);
+                    u32x4_t part[kParts];
+                    split_v(v, part);
 #pragma unroll
-                    for (int n = 0; n < PARTS; ++n)
+                    for (int n = 0; n < kParts; ++n)
                         *(u32x4_t*)(smem + (BN + n * BM + row) * 128 + ((c ^ turn_m(row)) << 4)) = part[n];
                 }
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < CB; ++j) {
-                    u32x4_t b[PARTS][2];
-#pragma unroll
-                    for (int n = 0; n < PARTS; ++n)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) b[n][h] = *(const u32x4_t*)(smem + n * BM * 128 + (at_m[j] ^ (64 * h)));
                     const bool on = mine[j] == a;
+#pragma unroll 1
+                    for (int h = 0; h < halves; ++h) {
+                        u32x4_t b[kParts];
 #pragma unroll
-                    for (int i = 0; i < RA; ++i) {
-                        f32x4_t d = zerof();
+                        for (int n = 0; n < kParts; ++n) b[n] = *(const u32x4_t*)(smem + n * BM * 128 + (at_m[j] ^ (64 * h)));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (h < halves) {
-                                const u32x4_t w = *(const u32x4_t*)(smem + (i / 4) * 64 * 128 + (at_n[i % 4] ^ (64 * h)));
+                        for (int i = 0; i < RA; ++i) {
+                            const u32x4_t w = *(const u32x4_t*)(smem + (i / 4) * 64 * 128 + (at_n[i % 4] ^ (64 * h)));
+                            f32x4_t d = zerof();
 #pragma unroll
-                                for (int n = 0; n < PARTS; ++n) d = mfma_bf16(w, b[n][h], d);
-                            }
+                            for (int n = 0; n < kParts; ++n) d = mfma_bf16(w, b[n], d);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = on ? acc[i][j][e] + d[e] : acc[i][j][e];
+                            for (int e = 0; e < 4; ++e) acc[i][j][e] = on ? acc[i][j][e] + d[e] : acc[i][j][e];
+                        }
                     }
                 }
                 __syncthreads();
