@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <string>
 
 #include "fp8.h"
 #include "lora.h"
@@ -684,6 +685,7 @@ void launch_shrink(const LoraArgs& p, int z, hipStream_t st) {
 template <typename OutT, typename BaseT>
 moe_status launch_stream(const LoraArgs& p, hipStream_t st) {
     const unsigned grid = (unsigned)((p.N + 15) / 16);
+    ProfScope ps(lora_alone(p) ? "lora_alone" : "lora_stream", st);
     if (lora_alone(p)) {
         lora_stream_kernel<OutT, BaseT, 1, 1><<<grid, 64 * kStreamWaves, 0, st>>>(p);
     } else if (p.M <= 16) lora_stream_kernel<OutT, BaseT, 1, 0><<<grid, 64 * kStreamWaves, 0, st>>>(p);
@@ -700,6 +702,9 @@ moe_status launch_tile(const LoraArgs& p, hipStream_t st) {
     constexpr int lds = R * (BN + BM) * 128;
     auto kern = lora_tile_kernel<OutT, BaseT, BN, BM, WN, WM, R>;
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+    // columns x rows, steps of the ring: a profile tells the tiles apart
+    static const std::string name = "lora_tile_" + std::to_string(BN) + "x" + std::to_string(BM) + "_" + std::to_string(R);
+    ProfScope ps(name.c_str(), st);
     kern<<<(unsigned)((tiles_of(p, BN, BM) + 7) / 8 * 8), 64 * WN * WM, lds, st>>>(p);
     return MOE_OK;
 }
@@ -707,6 +712,7 @@ moe_status launch_tile(const LoraArgs& p, hipStream_t st) {
 template <typename OutT, typename BaseT>
 moe_status launch_tiles(const LoraArgs& p, hipStream_t st) {
     if (!p.w) {
+        ProfScope ps("lora_add", st);
         lora_add_kernel<OutT, BaseT><<<dim3((unsigned)((p.N + kAddCols - 1) / kAddCols), (unsigned)((p.M + 63) / 64)), 256, 0, st>>>(p);
         return MOE_OK;
     }
@@ -755,7 +761,6 @@ moe_status lora_shrink(const LoraArgs& p, hipStream_t st) {
 }
 
 moe_status lora_rows(const LoraArgs& p, moe_dtype base, moe_dtype out, hipStream_t st) {
-    ProfScope ps(p.M <= kStreamRows ? "lora_stream" : p.w ? "lora_tile" : "lora_add", st);
     const moe_status e = out == MOE_BF16 ? launch_rows<uint16_t>(p, base, st) : launch_rows<float>(p, base, st);
     return e == MOE_OK ? check_launch("lora_rows") : e;
 }
