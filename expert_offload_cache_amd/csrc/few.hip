@@ -35,6 +35,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <string>
 
 #include "few_order.h"
 #include "ffn_common.h"
@@ -1106,6 +1107,10 @@ moe_status launch_shape(FewArgs a, hipStream_t st) {
     const int lds = a.choice_area + std::max({a.h_area + (W == MOE_FP8_B128 ? a.rows_fit * a.piece * CD * 4 : 0), sums, kWaves * RB * 1024});
     auto kern = few_layer_kernel<W, NS, RG, PB, RB, CD, RD, RE>;
     MOE_HIP(hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+    // weights, steps of x held, steps a chunk, row blocks a down item: a profile tells the forms apart
+    static const std::string name = std::string("few_layer_") + (W == MOE_F32 ? "f32" : W == MOE_BF16 ? "bf16" : W == MOE_INT4_G128 ? "int4" : "fp8") +
+                                    "_" + std::to_string(NS) + "_" + std::to_string(CD) + "_" + std::to_string(RB);
+    ProfScope ps(name.c_str(), st);
     // a workgroup a compute unit, fewer where there are fewer items
     const int64_t items = (int64_t)a.items_most * (a.f / 16 / PB) + a.d / 16 / RB * a.splits;
     kern<<<(unsigned)std::min<int64_t>(kFewUnits, items), kThreads, lds, st>>>(a);
@@ -1198,7 +1203,6 @@ extern "C" moe_status moe_layer_few(const void* x, moe_dtype act, int T, int d, 
     moe_status r = check_launch("few_prepare");
     if (r != MOE_OK) return r;
     const int rb = few_row_blocks(T, f, k, shared_w != nullptr, w);
-    ProfScope ps("few_layer", st);
     switch (w) {
         case MOE_F32: r = launch_layer<MOE_F32>(a, rb, st); break;
         case MOE_BF16: r = launch_layer<MOE_BF16>(a, rb, st); break;
