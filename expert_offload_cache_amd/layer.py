@@ -84,7 +84,7 @@ class DeviceLayer:
         return _new(stream, self.device, (n, torch.uint8), zero=True)[0]
 
     def buffers(self, T: int):
-        """Outputs of a T-token forward allocated once (a serving loop's buffers): forward(...,
+        """Outputs of a T-token forward allocated once (a serving loop's buffers), on the current stream: forward(...,
         bufs=...) writes into them, so each call overwrites the previous call's results."""
         import torch
 
