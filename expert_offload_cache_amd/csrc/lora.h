@@ -41,7 +41,7 @@ __device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) { return f32_to_
 // runs of the inputs whose sums launch 1 leaves
 constexpr size_t kLoraPartBytes = (size_t)1 << 20;
 int lora_splits(const LoraArgs& p);
-// one row and a low rank: v is formed by the launch that uses it
+// one row, a low rank and a workgroup a compute unit: v is formed by the launch that uses it
 bool lora_alone(const LoraArgs& p);
 // v = scale A x for the rows that have an adapter
 moe_status lora_shrink(const LoraArgs& p, hipStream_t st);

@@ -739,9 +739,15 @@ int lora_splits(const LoraArgs& p) {
     return (int)std::min<size_t>(splits, kLoraPartBytes / ((size_t)p.M * p.N * 4));
 }
 
-// One launch where its workgroups read little of A for themselves: 1 row of 4096 x 2048, rank 16, 9.2 us against 12.1 in
-// two launches; of 4096 x 4096, rank 32, 18.5 against 16.1.
-bool lora_alone(const LoraArgs& p) { return p.M == 1 && p.r <= 16; }
+// One launch or two for one row (us, N x K, one against two):
+//  - every workgroup of the one reads A for itself: rank 16, 4096 x 2048 9.6 against 11.5, 4096 x 4096 13.9 against 16.1; rank 32
+//    11.9 against 11.7, 18.1 against 16.1; rank 64 28 against 12;
+//  - so it has to be one workgroup a compute unit, 16 columns each: rank 16, 4096 x 2048 as above, 4112 x 2048 15.3 against 12.1,
+//    8192 x 2048 17.3 against 15.1, without W 4096 x 4096 8.5 against 9.2, 4608 x 4096 15.2 against 10.1;
+//  - a narrow W of long rows is better cut into runs of the inputs, which launch 1 of two does (lora_splits): rank 16,
+//    K = 4 N 1024 x 4096 13.1 against 13.4, 6 N 1024 x 6144 17.9 against 15.5, 8 N 1024 x 8192 21.8 against 18.2; without W
+//    1024 x 6144 10.4 against 11.4.
+bool lora_alone(const LoraArgs& p) { return p.M == 1 && p.r <= 16 && p.N <= 4096 && (!p.w || p.K <= (int64_t)4 * p.N); }
 
 moe_status lora_shrink(const LoraArgs& p, hipStream_t st) {
     if (lora_alone(p)) return MOE_OK;

@@ -33,6 +33,11 @@ CASES = [  # M, N, K, r, n, options of the inputs, launches
     (1, 300, 520, 16, 3, dict(none=0.0), {"lora_alone"}),
     (1, 300, 520, 24, 3, dict(none=0.0), {"lora_both", "lora_stream"}),
     (1, 300, 520, 8, 3, dict(w=False, base="f32", none=0.0), {"lora_alone"}),
+    (1, 4096, 264, 16, 3, dict(none=0.0), {"lora_alone"}),
+    (1, 4097, 264, 16, 3, dict(none=0.0), {"lora_both", "lora_stream"}),      # more workgroups than compute units
+    (1, 4097, 264, 16, 3, dict(w=False, base="bf16", none=0.0), {"lora_shrink", "lora_stream"}),
+    (1, 130, 1032, 16, 3, dict(none=0.0), {"lora_both", "lora_stream"}),      # long rows of a narrow matrix
+    (1, 130, 1032, 16, 3, dict(w=False, base="f32", none=0.0), {"lora_alone"}),
     (64, 4100, 264, 16, 3, dict(), {"lora_shrink", "lora_stream"}),  # more sums than launch 1's place holds
     (64, 1000, 2056, 72, 30, dict(), {"lora_both", "lora_stream"}),
     (64, 1000, 520, 72, 30, dict(w=False, base="bf16"), {"lora_shrink", "lora_stream"}),
