@@ -14,7 +14,7 @@
 // the sums.  A down item holds binary32 sums, so the gates are applied in registers and no rows are written between.
 //
 // What bounds it: the weights' bytes from 16 tokens on (2048 x 768, 8 of 128, bf16: 355 MB in 74 us, 4.8 TB/s; 4 bits,
-// 4096 x 2048, 6 of 256 + shared: 570 MB in 136 us); for one token latency (76 MB in 29 us: launch 1 takes 6, the selection
+// 4096 x 2048, 6 of 256 + shared: 570 MB in 138 us); for one token latency (76 MB in 29 us: launch 1 takes 5, the selection
 // 3.5, the first weights land 15 after the start, the join of y takes 2).
 //
 // The hand-over of h.  A down item needs h of every expert, which other workgroups write in the same

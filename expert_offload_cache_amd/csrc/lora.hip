@@ -130,8 +130,10 @@ __device__ __forceinline__ void stream_steps(int s0, int s1, int K, int q, Row&&
 
 // ---- launch 1 ---------------------------------------------------------------------------------------
 // A workgroup takes 16 * NM rows and NR blocks of 16 ranks; its NW waves split the inputs, each with the loads of C
-// steps on their way.  Bound by what a compute unit takes from its L2 (55 B/ns at most): 8192 rows of 4096, rank 32, 33 us
-// (512 KB each), rank 64, 47.  Of its rows' adapters it takes every Z-th.
+// steps on their way.  So x is read once for every 16 NR ranks and A once for every 16 NM rows: 8192 rows of 4096, rank 32, 33
+// us, rank 64, which reads x twice, 47.  A workgroup takes 512 KB there, 10 us at the most that a compute unit takes from its L2
+// (55 B/ns), and x alone 14 us from memory: with 16 steps a wave and 4 on their way it is latency that counts.
+// Of its rows' adapters a workgroup takes every Z-th.
 // red: NW * NM * NR KB of LDS.
 template <int NM, int NR, int NW, int C>
 __device__ __forceinline__ void shrink_tile(const LoraArgs& p, int m0, int r0, int z, int Z, float* red) {
@@ -311,7 +313,8 @@ struct Columns {
 // ALONE: one row whose v is formed here too, by every workgroup for itself (A is small and in L2: one launch less), by the
 // other 8 waves; NA blocks of 16 ranks.
 constexpr int kStreamWaves = 16;
-// Up to 64 rows (4 operand blocks, an element a thread at the end): 64 rows of 2048 x 4096 take 25 us, in tiles 131.
+// Up to 64 rows (4 operand blocks, an element a thread at the end): 64 rows of 2048 x 4096, rank 64, take 25.5 us, in tiles
+// 94; of 4096 x 2048, rank 16, 20.6 and 72.  So there is a step at 65 rows: nothing cuts the inputs of a 64 x 64 tile.
 constexpr int kStreamRows = 64;
 
 template <typename OutT, typename BaseT, int MB, int NA>
@@ -426,7 +429,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lora_stream_kernel(LoraArgs
 // A workgroup takes 64 rows and 512 columns, its 4 waves 64 columns at a time.  The rows' v lies in LDS as bf16 parts, 64
 // ranks at a time (row's chunk c at c ^ row % 8); B and base come straight to registers.  Columns in the order
 // of the tiles below, so that a lane holds 16 neighbouring ones.
-// 8192 rows of 4096, rank 64: 44 us, 134 MB of base and y at 3 TB/s.
+// 8192 rows of 4096, rank 64: 46 us, 134 MB of base and y at 2.9 TB/s.
 constexpr int kAddCols = 512;
 
 template <typename OutT, typename BaseT>
@@ -531,7 +534,7 @@ __global__ __launch_bounds__(256) void lora_add_kernel(LoraArgs p) {
 // position c ^ turn(row), so that no operand read meets a bank twice.
 // Operand row i of a wave's column block 4 g + b is column 64 g + 16 (i / 4) + 4 b + i % 4, so that a lane's results are
 // 16 neighbouring columns of a row, and four lanes' whole lines.
-// 8192 x 4096 x 4096: 260 us (1.06 PFLOP/s), the LDS reads take as long as the products; 1000 x 1001 x 2000: 21 us, latency.
+// 8192 x 4096 x 4096: 255 us (1.08 PFLOP/s), the LDS reads take as long as the products; 1000 x 1001 x 2000: 21 us, latency.
 // The adapters come last: each adapter of the tile's rows, 64 ranks at a time, with B and the parts of v in LDS in the
 // same layout, multiplied 32 ranks at a time: the registers hold one step's parts beside the tile's sums (both steps'
 // spill at 256 x 256: 308 us a call of 8192 x 4096 x 4096, rank 32, against 288).
@@ -716,8 +719,11 @@ moe_status launch_tiles(const LoraArgs& p, hipStream_t st) {
         lora_add_kernel<OutT, BaseT><<<dim3((unsigned)((p.N + kAddCols - 1) / kAddCols), (unsigned)((p.M + 63) / 64)), 256, 0, st>>>(p);
         return MOE_OK;
     }
-    // The largest tile that gives three quarters of the compute units one.  8192 x 4096 x 4096: 296 us in tiles of 256 x 256, 423
-    // in 128 x 128; 1000 x 1001 x 2000: 27 in 64 x 64, 52 in 128 x 128 (64 workgroups); 2048 x 4096 x 4096: 122 in 128 x 128.
+    // The largest tile that gives three quarters of the compute units one (us a call, outputs' columns x rows x inputs in
+    // tiles of 256 x 256, 128 x 128, 64 x 64): 4096 x 8192 x 4096, rank 32, 287, 435, 766; 4096 x 2944 x 4096 (192 of 256 x
+    // 256) 146, 173, 296; 4096 x 2048 x 4096 144, 130, 208; 2048 x 1536 x 4096 (192 of 128 x 128) 132, 69, 90; 1001 x 1000
+    // x 2000 (64 of 128 x 128) 101, 51, 27.  Below 192 of 128 x 128 the border depends on the inputs' length: 176 of
+    // them, 2048 x 1400 x 4096, 65 against 83 in 64 x 64.
     if (tiles_of(p, 256, 256) >= 192) return launch_tile<OutT, BaseT, 256, 256, 2, 4, 2>(p, st);
     if (tiles_of(p, 128, 128) >= 192) return launch_tile<OutT, BaseT, 128, 128, 2, 2, 3>(p, st);
     return launch_tile<OutT, BaseT, 64, 64, 1, 4, 6>(p, st);

@@ -340,7 +340,7 @@ MOE_API moe_status moe_gemm_fp8(const void* a, size_t lda, const float* a_scale,
  * ldx, ldw, ldb, ldy: elements from a row to the next.  K, r, ldx and ldw multiples of 8; x, w, a, b and ws start on
  * 16 bytes; any N; rows of base and y that start on 16 bytes are faster.  K up to 2^20, r up to MOE_LORA_MAX_RANK, N up to 2^22,
  * M up to 2^21, n up to 2^20.  y may be base (same type and stride); no other overlap.
- * Rows of one adapter next to each other are faster from 65 rows on (8192 rows of 12 adapters: 1.8 times a random order).
+ * Rows of one adapter next to each other are faster from 65 rows on (8192 rows of 12 adapters in a random order take 1.7 times as long).
  * ws: moe_lora_workspace_bytes(M, r) bytes, not initialised, one call at a time. */
 #define MOE_LORA_MAX_RANK 512
 /* grows with M and with r; 0 where the call refuses them */
