@@ -336,7 +336,7 @@ MOE_API moe_status moe_gemm_fp8(const void* a, size_t lda, const float* a_scale,
  *   adapter [M] int32; base [M,N] F32 or BF16; y [M,N] F32 or BF16, every row written, rounded once.
  * Sums are binary32; x A^T is kept in binary32 (from 65 rows on its second product takes it as a sum of bf16 parts, all
  * 24 bits of it).  The order of the sums follows from M, N, K and r.  Rows with infinities or NaN, and adapters with
- * them, touch no rows but their own; from 65 rows on an infinity in B gives NaN where it meets a finite x A^T, and an x A^T
+ * them, touch no rows but their own; from 65 rows on an infinity in B gives infinities or NaN where it meets a finite x A^T, and an x A^T
  * beyond the largest bf16 (3.39e38) counts as infinite.
  * ldx, ldw, ldb, ldy: elements from a row to the next.  K, r, ldx and ldw multiples of 8; x, w, a, b and ws start on
  * 16 bytes; any N; rows of base and y that start on 16 bytes are faster.  K up to 2^20, r up to MOE_LORA_MAX_RANK, N up to 2^22,
